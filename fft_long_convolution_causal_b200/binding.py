@@ -76,6 +76,24 @@ _SIGS = {
     "fftconv2d_fwd_dynamic": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp]),
     "fftconv_fwd_static_workspace": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fftconv_static_workspace_bytes": (ctypes.c_size_t, []),
+    "fftconv_linattn_plan_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                                                   ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]),
+    "fftconv_linattn_plan_destroy": (ctypes.c_int, [_vp]),
+    "fftconv_linattn_workspace_bytes": (ctypes.c_size_t, [_vp, ctypes.c_int]),
+    "fftconv_linattn_fwd": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+    "fftconv_linattn_bwd": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+    "fftconv_linattn_step": (ctypes.c_int, [_vp, _vp, _vp]),
+    "fftconv_linattn_set_wait_limit": (ctypes.c_int, [_vp, ctypes.c_uint32]),
+    "fftconv_linattn_device_status": (ctypes.c_int, [_vp, _vp]),
+    "fftconv_rotary_plan_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int, _vp]),
+    "fftconv_rotary_plan_destroy": (ctypes.c_int, [_vp]),
+    "fftconv_rotary_apply": (ctypes.c_int, [_vp, _vp, _vp]),
+    "fftconv_norm_plan_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                                ctypes.c_int, _vp]),
+    "fftconv_norm_plan_destroy": (ctypes.c_int, [_vp]),
+    "fftconv_norm_fwd": (ctypes.c_int, [_vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fftconv_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "fftconv_norm_bwd": (ctypes.c_int, [_vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fftconv_device_status": (ctypes.c_int, [_vp, _vp]),
     "fftconv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fftconv_version": (ctypes.c_int, []),

@@ -2,7 +2,8 @@
 
 ``python -m fft_long_convolution_causal_b200.build`` (or build()) compiles
 every .cu file under csrc/ into one shared library next to this file.  The
-library is rebuilt when any source or header is newer than it.
+library is rebuilt when any source or header is newer than it, from the objects
+whose own source and included files have not changed.
 """
 import glob
 import os
@@ -39,9 +40,21 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
-def _compile(src, verbose):
+def _fresh(obj) -> bool:
+    """The object is newer than every file its compilation read."""
+    try:
+        t = os.path.getmtime(obj)
+        deps = open(obj + ".d").read().split(":", 1)[1].replace("\\\n", " ").split()
+        return bool(deps) and all(os.path.getmtime(f) <= t for f in deps)
+    except (OSError, IndexError):
+        return False
+
+
+def _compile(src, verbose, force=True):
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj]
+    if not force and not verbose and _fresh(obj):
+        return obj, ""
+    cmd = [NVCC, *ARCH, *FLAGS, "-MD", "-MF", obj + ".d", "-c", src, "-o", obj]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -58,7 +71,7 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     srcs = _sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 1)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        results = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        results = list(ex.map(lambda s: _compile(s, verbose, force), srcs))
     if verbose:
         for _, log in results:
             sys.stderr.write(log)

@@ -1,0 +1,173 @@
+// rotary.cu -- rotary positions: pair i of a head turns by pos * f_i,
+//   y_1 = m (x_1 cos - x_2 sin),  y_2 = m (x_2 cos + x_1 sin),
+// (inverse: sin negated, the gradient of the rotation), the rest of the head copied.
+//
+// The angle is held in turns as a 64-bit fixed-point fraction: pos * f_i is an
+// integer product that wraps modulo one turn exactly, so a position of millions
+// costs no accuracy (the table's rounding, 2^-65 turn, times the position) and
+// no 64-bit floating-point arithmetic.  Its upper 32 bits give the sine and
+// cosine in fp32.
+//
+// Bound by memory (each element read and written once).  A thread owns some
+// pairs of one token, computes their sines once and walks a range of heads.
+#include <cuda_bf16.h>
+
+#include "mixer.h"
+
+namespace fftc {
+namespace rot {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;  // heads whose loads are in flight together
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int kN = 4;
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+struct Args {
+    RotaryView v[2];
+    int H, rot, dim, per_token, heads_per, inverse;
+    int64_t tokens, N, pos_stride;
+    const int64_t* pos;
+    const uint64_t* turns;
+    float m;
+};
+
+// V elements as one piece of memory (16 bytes, or one element)
+template <typename T, int V>
+struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Piece {
+    T e[V];
+};
+
+// V = elements of a 16-byte piece, or 1: an unaligned shape
+template <typename T, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Args a) {
+    using P = Piece<T, V>;
+    constexpr int NP = INTER && V > 1 ? V / 2 : V;  // pairs of an item
+    const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t token = idx / a.per_token;
+    if (token >= a.tokens) return;
+    const int item = (int)(idx - token * a.per_token);
+    const int64_t b = token / a.N, n = token - b * a.N;
+    const int h0 = blockIdx.y * a.heads_per, h1 = min(a.H, h0 + a.heads_per);
+    const int items = a.rot / 2 / NP;
+    auto from = [&](int h) -> const T* {
+        const RotaryView& w = a.v[h >= a.v[0].H];
+        return (const T*)w.x + b * w.xb + (h >= a.v[0].H ? h - a.v[0].H : h) * w.xh + n * w.xn;
+    };
+    auto to = [&](int h) -> T* {
+        const RotaryView& w = a.v[h >= a.v[0].H];
+        return (T*)w.y + b * w.yb + (h >= a.v[0].H ? h - a.v[0].H : h) * w.yh + n * w.yn;
+    };
+    if (item >= items) {  // behind the rotated part
+        const int e = a.rot + (item - items) * V;
+        for (int h = h0; h < h1; ++h) *reinterpret_cast<P*>(to(h) + e) = *reinterpret_cast<const P*>(from(h) + e);
+        return;
+    }
+    float cs[NP], sn[NP];
+    const uint64_t pos = (uint64_t)a.pos[b * a.pos_stride + n];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint64_t ph = pos * a.turns[item * NP + i];  // turns modulo 1, exactly
+        sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+        cs[i] *= a.m;
+        sn[i] *= a.inverse ? -a.m : a.m;
+    }
+    // offsets of the two pieces of an item; one piece when the pairs are neighbours
+    constexpr bool kOne = INTER && V > 1;
+    const int e0 = INTER ? 2 * NP * item : NP * item, e1 = INTER ? e0 + 1 : e0 + a.rot / 2;
+    for (int h = h0; h < h1; h += kAhead) {
+        P u[kAhead], w[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (h + k < h1) {
+                const T* x = from(h + k);
+                u[k] = *reinterpret_cast<const P*>(x + e0);
+                if (!kOne) w[k] = *reinterpret_cast<const P*>(x + e1);
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (h + k < h1) {
+                T* y = to(h + k);
+                P r = u[k], t = w[k];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const float x1 = to_f(kOne ? u[k].e[(2 * i) % V] : u[k].e[i % V]);
+                    const float x2 = to_f(kOne ? u[k].e[(2 * i + 1) % V] : w[k].e[i % V]);
+                    const T y1 = T(x1 * cs[i] - x2 * sn[i]), y2 = T(x2 * cs[i] + x1 * sn[i]);
+                    if (kOne) {
+                        r.e[(2 * i) % V] = y1;
+                        r.e[(2 * i + 1) % V] = y2;
+                    } else {
+                        r.e[i % V] = y1;
+                        t.e[i % V] = y2;
+                    }
+                }
+                *reinterpret_cast<P*>(y + e0) = r;
+                if (!kOne) *reinterpret_cast<P*>(y + e1) = t;
+            }
+    }
+}
+
+template <typename T, int V, bool INTER>
+cudaError_t run(Args a, int sms, bool copy_rest, cudaStream_t s) {
+    constexpr int NP = INTER && V > 1 ? V / 2 : V;
+    a.per_token = a.rot / 2 / NP + (copy_rest ? (a.dim - a.rot) / V : 0);
+    const int64_t threads = a.tokens * a.per_token;
+    // heads a thread walks: as many as leave the SMs full (the sines are then computed once for all)
+    int groups = (int)((int64_t)sms * 2048 / threads);
+    groups = groups < 1 ? 1 : groups > a.H ? a.H : groups;
+    a.heads_per = (a.H + groups - 1) / groups;
+    groups = (a.H + a.heads_per - 1) / a.heads_per;
+    rotary<T, V, INTER><<<dim3((unsigned)((threads + kThreads - 1) / kThreads), groups), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pick(const fftconv_rotary_s& p, Args& a, int views, cudaStream_t s) {
+    constexpr int V = Vec<T>::kN;
+    bool vec = a.dim % V == 0 && (p.interleaved ? a.rot % V == 0 : (a.rot / 2) % V == 0), rest = a.dim > a.rot;
+    bool same = true;
+    for (int i = 0; i < views; ++i) {
+        const RotaryView& v = a.v[i];
+        vec = vec && (((uintptr_t)v.x | (uintptr_t)v.y) & 15u) == 0 &&
+              ((v.xb | v.xh | v.xn | v.yb | v.yh | v.yn) % V) == 0;
+        same = same && v.x == v.y;
+    }
+    rest = rest && !same;
+    if (p.interleaved) return vec ? run<T, V, true>(a, p.sms, rest, s) : run<T, 1, true>(a, p.sms, rest, s);
+    return vec ? run<T, V, false>(a, p.sms, rest, s) : run<T, 1, false>(a, p.sms, rest, s);
+}
+
+}  // namespace rot
+
+cudaError_t launch_rotary(const fftconv_rotary_s& p, const RotaryView* v, int views, int B, int64_t N,
+                          const int64_t* pos, int64_t pos_stride, int inverse, cudaStream_t s) {
+    rot::Args a;
+    a.v[0] = v[0];
+    a.v[1] = views > 1 ? v[1] : v[0];
+    a.H = v[0].H + (views > 1 ? v[1].H : 0);
+    a.rot = p.rot;
+    a.dim = p.dim;
+    a.inverse = inverse;
+    a.tokens = (int64_t)B * N;
+    a.N = N;
+    a.pos = pos;
+    a.pos_stride = pos_stride;
+    a.turns = p.d_turns;
+    a.m = p.magnitude;
+    a.per_token = a.heads_per = 0;
+    return p.dtype == FFTCONV_BF16 ? rot::pick<__nv_bfloat16>(p, a, views, s) : rot::pick<float>(p, a, views, s);
+}
+
+}  // namespace fftc

@@ -452,6 +452,194 @@ FFTCONV_API size_t fftconv_static_workspace_bytes(void);
  */
 FFTCONV_API fftconv_status fftconv_device_status(fftconv_plan_t plan, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the convolution: linear attention with a decay per head,
+ * rotary positions and layer norm.  Linear attention is the input-dependent
+ * counterpart of the state-space filters above: its state decays like the
+ * filter k[t] = c a^t, and with rotated queries and keys its poles are
+ * a e^{i theta_j}, the lam_j of fftconv_ssm_plan_create.  No counterpart on
+ * the pages beyond that recurrence ("FlashConv", Mechanism: the state-space
+ * boundary state propagated between chunks).
+ *
+ * They follow this header's conventions (status codes, device pointers 16-byte
+ * aligned and owned by the caller, the plan's device current, work enqueued on
+ * the stream without synchronising) with these additions:
+ *   - B and N of a plan are the largest of a call; each call gives its own.
+ *   - Token tensors are strided views [B][H][N][d] whose last dimension is
+ *     contiguous; strides are in elements and multiples of 16 bytes.  An input
+ *     may have a stride of zero (a head shared by all); an output may not.
+ *   - Calls of one plan may run on several streams at once, each with its own
+ *     workspace (and distinct outputs).  Every call but plan creation,
+ *     destruction and *_device_status may be captured into a CUDA graph under
+ *     the condition given above.
+ *   - An argument block starts with its own size in bytes (size = sizeof);
+ *     unused pointers are NULL.
+ * ---------------------------------------------------------------------- */
+typedef struct fftconv_linattn_s fftconv_linattn;
+typedef struct fftconv_rotary_s fftconv_rotary;
+typedef struct fftconv_norm_s fftconv_norm;
+
+typedef struct {
+    int64_t batch, head, token;
+} fftconv_strides;
+
+/*
+ * Linear attention with a decay a_h = exp(log_decay[h]) for each head:
+ *     S_t = a_h S_{t-1} + k_t^T v_t,    o_t = scale q_t S_t
+ * q, k: [B][H][N][dk], v, o: [B][H][N][dv] of the plan's dtype; the state S
+ * [dk][dv] in fp32, S_{-1} = state_in or zero.  dk and dv are multiples of 8
+ * in [8, FFTCONV_LINATTN_MAX_DIM].  log_decay is a host array of H values
+ * <= 0 (minus infinity: only the token itself), constants of the plan.  bf16
+ * products accumulate in fp32; the scores and the state's copy read by q are
+ * rounded to bf16 once, the state itself is not.
+ * FFTCONV_ERR_UNSUPPORTED for other dims or B H > 65535.
+ */
+#define FFTCONV_LINATTN_MAX_DIM 128
+FFTCONV_API fftconv_status fftconv_linattn_plan_create(fftconv_linattn** plan, int B, int H, int64_t N, int dk,
+                                                       int dv, fftconv_dtype dtype, const double* log_decay);
+FFTCONV_API fftconv_status fftconv_linattn_plan_destroy(fftconv_linattn* plan);
+/* Device workspace of any fftconv_linattn_fwd (backward = 0) or _bwd (1) call of the plan. */
+FFTCONV_API size_t fftconv_linattn_workspace_bytes(const fftconv_linattn* plan, int backward);
+
+typedef struct {
+    size_t size;
+    int B;
+    int64_t N;
+    double scale;
+    const void *q, *k, *v;
+    fftconv_strides sq, sk, sv;
+    const int32_t* lengths;  /* [B] on the device or NULL: tokens of each row, clamped to [0, N]  */
+    const float* state_in;   /* [B][H][dk][dv] or NULL                                            */
+    void* o;                 /* rows at or behind a length are not read and written as zeros     */
+    fftconv_strides so;
+    float* state_out;        /* [B][H][dk][dv]: the state after each row's last token; or NULL;   */
+                             /* may be state_in                                                   */
+} fftconv_linattn_args;
+
+/* Forward over whole prompts, in chunks.  A NaN or infinity in a live token
+ * may reach every token of its row's chunk (up to 128 tokens) and all later
+ * ones; rows behind a length never do. */
+FFTCONV_API fftconv_status fftconv_linattn_fwd(const fftconv_linattn* plan, const fftconv_linattn_args* args,
+                                               void* workspace, void* stream);
+
+typedef struct {
+    size_t size;
+    int B;
+    int64_t N;
+    double scale;
+    const void *d_o, *q, *k, *v;
+    fftconv_strides sdo, sq, sk, sv;
+    const int32_t* lengths;
+    const float* state_in;   /* the forward's, or NULL                                            */
+    const float* d_state;    /* gradient of state_out [B][H][dk][dv], or NULL (zero)             */
+    void *dq, *dk, *dv;      /* zeros at or behind a length                                       */
+    fftconv_strides sdq, sdk, sdv;
+    float* d_state_in;       /* gradient of state_in [B][H][dk][dv], or NULL; no alias           */
+} fftconv_linattn_bwd_args;
+
+/* Backward: with R_t = a R_{t+1} + scale q_t^T do_t (R behind the last token:
+ * d_state), dq_t = scale do_t S_t^T, dk_t = R_t v_t, dv_t = k_t R_t and
+ * d_state_in = a R_0.  S is recomputed; nothing is kept by the forward. */
+FFTCONV_API fftconv_status fftconv_linattn_bwd(const fftconv_linattn* plan, const fftconv_linattn_bwd_args* args,
+                                               void* workspace, void* stream);
+
+typedef struct {
+    size_t size;
+    int B;
+    int slots_n;             /* states in the pool                                                */
+    double scale;
+    const void *q, *k, *v;   /* [B][H][d], strides in elements (token unused), any alignment      */
+    fftconv_strides sq, sk, sv;
+    const int32_t* slots;    /* [B] on the device: the state of each row; NULL: row b has state b */
+    float* state;            /* [slots_n][H][dk][dv], updated in place                            */
+    void* o;                 /* [B][H][dv]                                                        */
+    fftconv_strides so;
+} fftconv_linattn_step_args;
+
+/* One token a row, the recurrent form.  A row whose slot is outside
+ * [0, slots_n) is idle: zeros in o, no state touched.  Rows that name one slot
+ * are taken in row order. */
+FFTCONV_API fftconv_status fftconv_linattn_step(const fftconv_linattn* plan, const fftconv_linattn_step_args* args,
+                                                void* stream);
+
+/* As fftconv_plan_set_wait_limit and fftconv_device_status, for a linear-attention plan. */
+FFTCONV_API fftconv_status fftconv_linattn_set_wait_limit(fftconv_linattn* plan, uint32_t probes);
+FFTCONV_API fftconv_status fftconv_linattn_device_status(fftconv_linattn* plan, void* stream);
+
+/*
+ * Rotary positions: pair i of the first rot elements of a head of dim elements
+ * turns by position * f_i,
+ *     y_1 = m (x_1 cos - x_2 sin),   y_2 = m (x_2 cos + x_1 sin),
+ * the pair being (i, i + rot / 2) (half layout) or (2 i, 2 i + 1)
+ * (interleaved); elements behind rot are copied.  f_i = base^(-2 i / rot), and
+ *   FFTCONV_ROTARY_LINEAR  f_i / factor;
+ *   FFTCONV_ROTARY_BASE    base factor^(rot / (rot - 2)) for the base (rot >= 4);
+ *   FFTCONV_ROTARY_PARTS   pairs that turn more than 32 times over `context`
+ *                          positions keep f_i, those that turn less than once
+ *                          take f_i / factor, a linear ramp over i between
+ *                          (its ends rounded outwards to whole pairs);
+ *                          m = 0.1 ln(factor) + 1.
+ * m = 1 otherwise.  Angles are exact modulo a turn for any 64-bit position.
+ */
+typedef enum {
+    FFTCONV_ROTARY_NONE = 0,
+    FFTCONV_ROTARY_LINEAR = 1,
+    FFTCONV_ROTARY_BASE = 2,
+    FFTCONV_ROTARY_PARTS = 3
+} fftconv_rotary_scaling;
+
+typedef struct {
+    size_t size;
+    int dim, rot;            /* 2 <= rot <= dim <= FFTCONV_ROTARY_MAX_DIM, rot even               */
+    int interleaved;
+    int scaling;             /* fftconv_rotary_scaling                                            */
+    double base, factor;     /* base > 1, factor >= 1                                             */
+    double context;          /* FFTCONV_ROTARY_PARTS: positions trained on, > 0                   */
+} fftconv_rotary_options;
+
+#define FFTCONV_ROTARY_MAX_DIM 1024
+FFTCONV_API fftconv_status fftconv_rotary_plan_create(fftconv_rotary** plan, fftconv_dtype dtype,
+                                                      const fftconv_rotary_options* options);
+FFTCONV_API fftconv_status fftconv_rotary_plan_destroy(fftconv_rotary* plan);
+
+typedef struct {
+    size_t size;
+    int B;
+    int64_t N;
+    int H, H2;               /* heads of x and of x2 (0: no x2)                                   */
+    const int64_t* positions;        /* [B][N] on the device, or [N] with position_stride 0      */
+    int64_t position_stride;         /* between rows                                              */
+    int inverse;             /* the rotation by the negated angle, times m: the gradient         */
+    const void *x, *x2;      /* [B][H][N][dim], strides any multiple of an element                */
+    void *y, *y2;            /* may be x, x2 with the same strides                                */
+    fftconv_strides sx, sx2, sy, sy2;
+} fftconv_rotary_args;
+
+FFTCONV_API fftconv_status fftconv_rotary_apply(const fftconv_rotary* plan, const fftconv_rotary_args* args,
+                                                void* stream);
+
+/*
+ * Layer norm over rows of C elements, 1 <= C <= FFTCONV_NORM_MAX_C:
+ *     y = (x - mean) rstd w + b,   rstd = 1 / sqrt(var + eps)
+ * x, y: [rows][C] dense, of the plan's dtype; w, b: [groups][C] fp32, row r
+ * uses row r mod groups (1: one weight; the number of heads: the norm behind
+ * each head of [..][heads][C]).  Statistics in fp32.  `rows` of a call is at
+ * most the plan's and a multiple of groups.
+ */
+#define FFTCONV_NORM_MAX_C 16384
+FFTCONV_API fftconv_status fftconv_norm_plan_create(fftconv_norm** plan, int64_t rows, int C, int groups,
+                                                    fftconv_dtype dtype, const double* eps);
+FFTCONV_API fftconv_status fftconv_norm_plan_destroy(fftconv_norm* plan);
+/* mean, rstd: [rows] fp32 for the backward pass, or NULL.  y may be x. */
+FFTCONV_API fftconv_status fftconv_norm_fwd(const fftconv_norm* plan, int64_t rows, const void* x, const float* w,
+                                            const float* b, void* y, float* mean, float* rstd, void* stream);
+/* Device workspace of fftconv_norm_bwd. */
+FFTCONV_API size_t fftconv_norm_bwd_workspace_bytes(const fftconv_norm* plan);
+/* dx [rows][C] (may be dy), dw and db [groups][C] fp32, summed in a fixed order. */
+FFTCONV_API fftconv_status fftconv_norm_bwd(const fftconv_norm* plan, int64_t rows, const void* dy, const void* x,
+                                            const float* w, const float* mean, const float* rstd, void* dx,
+                                            float* dw, float* db, void* workspace, void* stream);
+
 /* Human-readable name of a status code (static string). */
 FFTCONV_API const char* fftconv_status_string(fftconv_status status);
 
