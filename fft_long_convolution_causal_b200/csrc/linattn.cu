@@ -8,13 +8,13 @@
 //   dq = pass(do, v, k) forward, dk = pass(v, do, q) and dv = pass(k, q, do) in reverse.
 // Every exponent is >= 0, so nothing overflows however strong the decay is.
 //
-// The token axis is cut into segments where one CTA per (row, head) would leave
+// bf16 runs on the tensor cores (linattn_tc.cu), fp32 here.  The token axis is cut into segments where one CTA per (row, head) would leave
 // SMs idle: a first kernel sums each segment's own contribution to the state, a
 // second carries the states over the segments, the third computes the outputs.
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include "mixer.h"
+#include "linattn.cuh"
 
 namespace fftc {
 namespace la {
@@ -25,21 +25,8 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// four consecutive elements as fp32
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    uint2 u;
-    u.x = *reinterpret_cast<uint32_t*>(&a);
-    u.y = *reinterpret_cast<uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = u;
-}
 
 template <int DX, int DZ>
 struct Shape {
@@ -48,8 +35,8 @@ struct Shape {
 };
 
 // rows [t0, t0 + kC) of a tensor into shared memory as fp32, zeros behind row `live` and column d
-template <typename T, int D, int P>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stride, int live, int d) {
+template <int D, int P>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t stride, int live, int d) {
     for (int e = threadIdx.x; e < kC * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = 4 * (e % (D / 4));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -58,24 +45,8 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stri
     }
 }
 
-struct Args {
-    LaPass p[kLaMaxPasses];
-    int H, nseg;
-    int64_t N, seg;             // tokens, tokens a segment
-    const int32_t* lengths;
-    const float* pw;            // [H][kLaPowers]
-    float* work;                // [pass][bh][nseg][dk * dv]: segment states
-    size_t pass_floats, state_floats;
-};
-
-__device__ __forceinline__ int64_t live_tokens(const Args& a, int b) {
-    if (!a.lengths) return a.N;
-    const int64_t n = a.lengths[b];
-    return n < 0 ? 0 : n > a.N ? a.N : n;
-}
-
 // grid (segments, rows x heads, passes); STATES: only the segments' own states
-template <typename T, int DX, int DZ, bool STATES>
+template <int DX, int DZ, bool STATES>
 __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args a) {
     using S = Shape<DX, DZ>;
     extern __shared__ __align__(16) float sm[];
@@ -87,10 +58,10 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
     const int64_t first = sg * a.seg, len = live_tokens(a, b);
     const int64_t rows = min(a.seg, a.N - first);                   // output rows of this segment
     const int64_t live = max((int64_t)0, min(rows, len - first));   // of which read
-    const T* x = (const T*)p.x + b * p.sx.batch + h * p.sx.head + first * p.sx.token;
-    const T* y = (const T*)p.y + b * p.sy.batch + h * p.sy.head + first * p.sy.token;
-    const T* z = (const T*)p.z + b * p.sz.batch + h * p.sz.head + first * p.sz.token;
-    T* out = (T*)p.out + b * p.so.batch + h * p.so.head + first * p.so.token;
+    const float* x = (const float*)p.x + b * p.sx.batch + h * p.sx.head + first * p.sx.token;
+    const float* y = (const float*)p.y + b * p.sy.batch + h * p.sy.head + first * p.sy.token;
+    const float* z = (const float*)p.z + b * p.sz.batch + h * p.sz.head + first * p.sz.token;
+    float* out = (float*)p.out + b * p.so.batch + h * p.so.head + first * p.so.token;
     float* wseg = a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats;
     for (int i = tid; i < kLaPowers; i += kThreads) pw[i] = a.pw[h * kLaPowers + i];
     // the state entering the segment
@@ -105,9 +76,9 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
         const int64_t t0 = (int64_t)(p.reverse ? nch - 1 - ch : ch) * kC;
         const int L = (int)min((int64_t)kC, live - t0);
         __syncthreads();
-        if (!STATES) load_tile<T, DX, S::PX>(xs, x + t0 * p.sx.token, p.sx.token, L, p.dx);
-        load_tile<T, DX, S::PX>(ys, y + t0 * p.sy.token, p.sy.token, L, p.dx);
-        load_tile<T, DZ, S::PZ>(zs, z + t0 * p.sz.token, p.sz.token, L, p.dz);
+        if (!STATES) load_tile<DX, S::PX>(xs, x + t0 * p.sx.token, p.sx.token, L, p.dx);
+        load_tile<DX, S::PX>(ys, y + t0 * p.sy.token, p.sy.token, L, p.dx);
+        load_tile<DZ, S::PZ>(zs, z + t0 * p.sz.token, p.sz.token, L, p.dz);
         __syncthreads();
         if (!STATES) {
             float acc[4][4] = {};
@@ -232,31 +203,27 @@ __global__ void la_carry(const __grid_constant__ Args a, const double* __restric
     if (p.s_out) p.s_out[(size_t)bh * n + e] = s;
 }
 
-template <typename T, int DX, int DZ>
-cudaError_t run(const Args& a, int bh, int passes, const double* lg, cudaStream_t s) {
+template <int DX, int DZ>
+cudaError_t run(const Args& a, int bh, int passes, bool states, cudaStream_t s) {
     constexpr int bytes = Shape<DX, DZ>::kFloats * (int)sizeof(float);
     static bool once = false;
     if (!once) {
-        cudaFuncSetAttribute(la_simt<T, DX, DZ, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        cudaFuncSetAttribute(la_simt<T, DX, DZ, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncSetAttribute(la_simt<DX, DZ, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncSetAttribute(la_simt<DX, DZ, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         once = true;
     }
     const dim3 grid(a.nseg, bh, passes);
-    cudaError_t e;
-    if (a.nseg > 1) {
-        la_simt<T, DX, DZ, true><<<grid, kThreads, bytes, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        la_carry<<<dim3((unsigned)((a.state_floats + 255) / 256), bh, passes), 256, 0, s>>>(a, lg);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    la_simt<T, DX, DZ, false><<<grid, kThreads, bytes, s>>>(a);
+    if (states)
+        la_simt<DX, DZ, true><<<grid, kThreads, bytes, s>>>(a);
+    else
+        la_simt<DX, DZ, false><<<grid, kThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t pick(const Args& a, int dx, int dz, int bh, int passes, const double* lg, cudaStream_t s) {
-    if (dx <= 64) return dz <= 64 ? run<T, 64, 64>(a, bh, passes, lg, s) : run<T, 64, 128>(a, bh, passes, lg, s);
-    return dz <= 64 ? run<T, 128, 64>(a, bh, passes, lg, s) : run<T, 128, 128>(a, bh, passes, lg, s);
+cudaError_t launch_simt(const Args& a, int dx, int dz, int bh, int passes, bool states, cudaStream_t s) {
+    if (dx <= 64)
+        return dz <= 64 ? run<64, 64>(a, bh, passes, states, s) : run<64, 128>(a, bh, passes, states, s);
+    return dz <= 64 ? run<128, 64>(a, bh, passes, states, s) : run<128, 128>(a, bh, passes, states, s);
 }
 
 // one CTA per (row, head), its state in registers between the read and the write
@@ -342,44 +309,80 @@ la_step(const LaStep c, int H, int dk, int dv, const float* __restrict__ pw) {
 
 }  // namespace la
 
-// One CTA per (segment, row, head, pass): as many segments as fill the SMs twice.
-int la_segments(const fftconv_linattn_s& p, int B, int64_t N, int passes) {
-    const int64_t chunks = (N + kLaChunk - 1) / kLaChunk;
-    const int64_t ctas = (int64_t)B * p.H * passes;
-    int64_t n = (2 * p.sms) / (ctas > 0 ? ctas : 1);
-    if (n < 1) n = 1;
-    if (n > kLaMaxSegments) n = kLaMaxSegments;
-    if (n > chunks) n = chunks;
-    return (int)n;
+namespace {
+
+// dk and dv padded to one shape for every pass of the call
+void padded(const fftconv_linattn_s& p, int passes, int* dx, int* dz) {
+    *dx = passes == 1 ? p.dk : (p.dk > p.dv ? p.dk : p.dv);
+    *dz = passes == 1 ? p.dv : *dx;
 }
 
+int chunk_of(const fftconv_linattn_s& p) { return p.dtype == FFTCONV_BF16 ? kLaChunkTc : kLaChunk; }
+
+// CTAs the GPU holds at once: two an SM where both dims fit 64
+int64_t slots_of(const fftconv_linattn_s& p, int passes) {
+    int dx, dz;
+    padded(p, passes, &dx, &dz);
+    return (int64_t)p.sms * (dx <= 64 && dz <= 64 ? 2 : 1);
+}
+
+// Segments the token axis is cut into.  In units of one chunk's time, a CTA
+// costs its chunks and about 1.5 to start; more than one segment adds the pass
+// over the segments' own states (two tensors of four: about 0.6 a chunk) and
+// the launch that joins them.
+int segments(const fftconv_linattn_s& p, int B, int64_t N, int passes) {
+    const int64_t chunks = (N + chunk_of(p) - 1) / chunk_of(p), ctas = (int64_t)B * p.H * passes;
+    const int64_t slots = slots_of(p, passes);
+    int best = 1;
+    double least = 0.0;
+    for (int n = 1; n <= kLaMaxSegments && n <= chunks && (n == 1 || ctas * n <= kLaMaxWaves * slots); ++n) {
+        const int64_t per = (chunks + n - 1) / n, waves = (ctas * n + slots - 1) / slots;
+        if (n > 1 && (chunks + per - 1) / per != n) continue;  // an empty segment
+        const double cost = waves * (per + 1.5) + (n > 1 ? waves * (0.6 * per + 1.0) + 3.0 : 0.0);
+        if (n == 1 || cost < least) {
+            best = n;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 size_t la_workspace_floats(const fftconv_linattn_s& p, int passes) {
-    // the largest over every B and N of the plan: segments x rows x heads x passes never exceeds
-    // the larger of twice the SMs and one segment each (which needs none)
-    (void)passes;
-    return (size_t)2 * p.sms * p.dk * p.dv;
+    // enough for every B and N up to the plan's: segments times CTAs is bounded above
+    const int64_t chunks = (p.N + chunk_of(p) - 1) / chunk_of(p);
+    if (chunks == 1) return 0;
+    const int64_t most = (int64_t)p.B * p.H * passes * (chunks < kLaMaxSegments ? chunks : kLaMaxSegments);
+    const int64_t cap = kLaMaxWaves * slots_of(p, passes);
+    return (size_t)(most < cap ? most : cap) * p.dk * p.dv;
 }
 
 cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t s) {
+    const int64_t chunk = chunk_of(p), chunks = (c.N + chunk - 1) / chunk;
     la::Args a;
     for (int i = 0; i < c.passes; ++i) a.p[i] = c.pass[i];
     a.H = p.H;
-    a.nseg = la_segments(p, c.B, c.N, c.passes);
-    const int64_t chunks = (c.N + kLaChunk - 1) / kLaChunk;
-    a.seg = (chunks + a.nseg - 1) / a.nseg * kLaChunk;
-    a.nseg = (int)((c.N + a.seg - 1) / a.seg);
+    a.nseg = segments(p, c.B, c.N, c.passes);
+    a.seg = (chunks + a.nseg - 1) / a.nseg * chunk;
     a.N = c.N;
     a.lengths = c.lengths;
     a.pw = p.d_pow;
     a.work = c.work;
     a.state_floats = (size_t)p.dk * p.dv;
     a.pass_floats = (size_t)c.B * p.H * a.nseg * a.state_floats;
-    // dk and dv padded to one shape for every pass of the call
-    const int dx = c.passes == 1 ? c.pass[0].dx : (p.dk > p.dv ? p.dk : p.dv);
-    const int dz = c.passes == 1 ? c.pass[0].dz : dx;
+    int dx, dz;
+    padded(p, c.passes, &dx, &dz);
     const int bh = c.B * p.H;
-    return p.dtype == FFTCONV_BF16 ? la::pick<__nv_bfloat16>(a, dx, dz, bh, c.passes, p.d_log, s)
-                                   : la::pick<float>(a, dx, dz, bh, c.passes, p.d_log, s);
+    const bool tc = p.dtype == FFTCONV_BF16;
+    if (a.nseg > 1) {
+        cudaError_t e = tc ? la::launch_tc_states(a, dx, dz, bh, c.passes, p, s)
+                           : la::launch_simt(a, dx, dz, bh, c.passes, true, s);
+        if (e != cudaSuccess) return e;
+        la::la_carry<<<dim3((unsigned)((a.state_floats + 255) / 256), bh, c.passes), 256, 0, s>>>(a, p.d_log);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return tc ? la::launch_tc_main(a, dx, dz, bh, c.passes, p, s) : la::launch_simt(a, dx, dz, bh, c.passes, false, s);
 }
 
 cudaError_t launch_la_step(const fftconv_linattn_s& p, const LaStep& c, cudaStream_t s) {

@@ -51,9 +51,11 @@ struct LaPass {
     float s_p, s_i, s_u;
 };
 
-constexpr int kLaChunk = 64;      // tokens a step of the SIMT kernel
+constexpr int kLaChunk = 64;      // tokens a step of the fp32 kernel
+constexpr int kLaChunkTc = 128;   // and of the tensor-core kernel
 constexpr int kLaPowers = 132;    // table length per head (exponents 0 .. 128, padded)
 constexpr int kLaMaxSegments = 64;
+constexpr int kLaMaxWaves = 4;    // segments times CTAs, over what the GPU holds at once
 constexpr int kLaMaxPasses = 3;
 
 struct LaCall {
@@ -65,8 +67,7 @@ struct LaCall {
     float* work;                      // segment states
 };
 
-// Segments of the token axis a call is split into, and its workspace in floats.
-int la_segments(const fftconv_linattn_s& p, int B, int64_t N, int passes);
+// Workspace of a call of that many passes, in floats.
 size_t la_workspace_floats(const fftconv_linattn_s& p, int passes);
 cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t s);
 
