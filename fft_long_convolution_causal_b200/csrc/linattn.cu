@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
     float* wseg = a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats;
     for (int i = tid; i < kLaPowers; i += kThreads) pw[i] = a.pw[h * kLaPowers + i];
     // the state entering the segment
-    const float* s0 = STATES ? nullptr : a.nseg > 1 ? wseg : p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
-    const bool trans = a.nseg == 1 && p.in_trans;
+    const float* s0 = STATES ? nullptr : p.carried ? wseg : p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
+    const bool trans = !p.carried && p.in_trans;
     for (int e = tid; e < DX * DZ; e += kThreads) {
         const int d = e / DZ, n = e % DZ;
         ss[d * S::PZ + n] = s0 && d < p.dx && n < p.dz ? s0[trans ? n * p.dx + d : d * p.dz + n] : 0.f;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
         }
     }
     __syncthreads();
-    float* so = STATES ? wseg : a.nseg == 1 && p.s_out ? p.s_out + (size_t)bh * p.dx * p.dz : nullptr;
+    float* so = STATES ? wseg : !p.carried && p.s_out ? p.s_out + (size_t)bh * p.dx * p.dz : nullptr;
     if (so)
         for (int e = tid; e < p.dx * p.dz; e += kThreads) so[e] = ss[(e / p.dz) * S::PZ + e % p.dz];
     if (!STATES)  // rows behind the sequence
@@ -183,35 +183,61 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
 }
 
 // Replaces each segment's own state by the state entering it, in the order the
-// pass runs, and writes the last one out; one thread per element.
-__global__ void la_carry(const __grid_constant__ Args a, const double* __restrict__ lg) {
+// pass runs, and writes the last one out; a thread per four elements, the loads
+// of eight segments in flight together.
+constexpr int kCarryThreads = 128;
+__global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant__ Args a, const double* __restrict__ lg) {
     const LaPass& p = a.p[blockIdx.z];
-    const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, e = blockIdx.x * blockDim.x + threadIdx.x;
-    const int n = p.dx * p.dz;
-    if (e >= n) return;
+    if (!p.carried) return;
+    __shared__ float decay[kLaMaxSegments];  // over a segment; below zero: an empty one
+    const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, n = p.dx * p.dz;
     const int64_t len = live_tokens(a, b);
-    float* w = a.work + blockIdx.z * a.pass_floats + (size_t)bh * a.nseg * a.state_floats + e;
-    float s = p.s_in ? p.s_in[(size_t)bh * n + (p.in_trans ? (e % p.dz) * p.dx + e / p.dz : e)] : 0.f;
-    for (int k = 0; k < a.nseg; ++k) {
+    for (int k = threadIdx.x; k < a.nseg; k += kCarryThreads) {
         const int sg = p.reverse ? a.nseg - 1 - k : k;
-        const int64_t live = max((int64_t)0, min(a.seg, len - sg * a.seg));
-        const float own = w[sg * a.state_floats];
-        w[sg * a.state_floats] = s;
-        // an empty segment passes the state on (its decay's exponent is 0 even for a decay of zero)
-        if (live > 0) s = (float)exp(lg[h] * (double)live) * s + own;
+        const int64_t live = min(a.seg, len - sg * a.seg);
+        // an empty segment passes the state on (also where the decay is zero)
+        decay[k] = live > 0 ? (float)exp(lg[h] * (double)live) : -1.f;
     }
-    if (p.s_out) p.s_out[(size_t)bh * n + e] = s;
+    __syncthreads();
+    const int e = 4 * (blockIdx.x * kCarryThreads + threadIdx.x);
+    if (e >= n) return;
+    float* w = a.work + blockIdx.z * a.pass_floats + (size_t)bh * a.nseg * a.state_floats + e;
+    const int64_t step = (p.reverse ? -1 : 1) * (int64_t)a.state_floats;
+    if (p.reverse) w += (a.nseg - 1) * a.state_floats;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.s_in) {
+        const float* q = p.s_in + (size_t)bh * n;
+        if (p.in_trans) {
+            const int d = e / p.dz, c = e % p.dz;
+            s = make_float4(q[c * p.dx + d], q[(c + 1) * p.dx + d], q[(c + 2) * p.dx + d], q[(c + 3) * p.dx + d]);
+        } else {
+            s = load4(q + e);
+        }
+    }
+    for (int k0 = 0; k0 < a.nseg; k0 += 8) {
+        float4 own[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k0 + i < a.nseg) own[i] = load4(w + (k0 + i) * step);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k0 + i < a.nseg) {
+                const float f = decay[k0 + i];
+                store4(w + (k0 + i) * step, s);
+                if (f >= 0.f) {
+                    s.x = fmaf(f, s.x, own[i].x), s.y = fmaf(f, s.y, own[i].y);
+                    s.z = fmaf(f, s.z, own[i].z), s.w = fmaf(f, s.w, own[i].w);
+                }
+            }
+    }
+    if (p.s_out) store4(p.s_out + (size_t)bh * n + e, s);
 }
 
 template <int DX, int DZ>
 cudaError_t run(const Args& a, int bh, int passes, bool states, cudaStream_t s) {
     constexpr int bytes = Shape<DX, DZ>::kFloats * (int)sizeof(float);
-    static bool once = false;
-    if (!once) {
-        cudaFuncSetAttribute(la_simt<DX, DZ, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        cudaFuncSetAttribute(la_simt<DX, DZ, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        once = true;
-    }
+    const cudaError_t e = states ? allow<la_simt<DX, DZ, true>>(bytes) : allow<la_simt<DX, DZ, false>>(bytes);
+    if (e != cudaSuccess) return e;
     const dim3 grid(a.nseg, bh, passes);
     if (states)
         la_simt<DX, DZ, true><<<grid, kThreads, bytes, s>>>(a);
@@ -350,18 +376,17 @@ int segments(const fftconv_linattn_s& p, int B, int64_t N, int passes) {
 }  // namespace
 
 size_t la_workspace_floats(const fftconv_linattn_s& p, int passes) {
-    // enough for every B and N up to the plan's: segments times CTAs is bounded above
-    const int64_t chunks = (p.N + chunk_of(p) - 1) / chunk_of(p);
-    if (chunks == 1) return 0;
-    const int64_t most = (int64_t)p.B * p.H * passes * (chunks < kLaMaxSegments ? chunks : kLaMaxSegments);
-    const int64_t cap = kLaMaxWaves * slots_of(p, passes);
-    return (size_t)(most < cap ? most : cap) * p.dk * p.dv;
+    // enough for every B and N up to the plan's: one state a CTA, and the bound on segments times CTAs
+    const int64_t chunks = (p.N + chunk_of(p) - 1) / chunk_of(p), ctas = (int64_t)p.B * p.H * passes;
+    const int64_t most = ctas * (chunks < kLaMaxSegments ? chunks : kLaMaxSegments), cap = kLaMaxWaves * slots_of(p, passes);
+    const int64_t states = most < cap ? most : cap > ctas ? cap : ctas;
+    return (size_t)states * p.dk * p.dv;
 }
 
 cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t s) {
     const int64_t chunk = chunk_of(p), chunks = (c.N + chunk - 1) / chunk;
+    const bool tc = p.dtype == FFTCONV_BF16;
     la::Args a;
-    for (int i = 0; i < c.passes; ++i) a.p[i] = c.pass[i];
     a.H = p.H;
     a.nseg = segments(p, c.B, c.N, c.passes);
     a.seg = (chunks + a.nseg - 1) / a.nseg * chunk;
@@ -371,18 +396,26 @@ cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t 
     a.work = c.work;
     a.state_floats = (size_t)p.dk * p.dv;
     a.pass_floats = (size_t)c.B * p.H * a.nseg * a.state_floats;
+    bool carried = false;
+    for (int i = 0; i < c.passes; ++i) {
+        a.p[i] = c.pass[i];
+        // the tensor-core outputs' kernel keeps its state for the outputs alone: states that a caller
+        // asks for come from the states' kernel, which sums them in fp32
+        a.p[i].carried = a.nseg > 1 || (tc && a.p[i].s_out);
+        carried = carried || a.p[i].carried;
+    }
     int dx, dz;
     padded(p, c.passes, &dx, &dz);
     const int bh = c.B * p.H;
-    const bool tc = p.dtype == FFTCONV_BF16;
-    if (a.nseg > 1) {
-        cudaError_t e = tc ? la::launch_tc_states(a, dx, dz, bh, c.passes, p, s)
-                           : la::launch_simt(a, dx, dz, bh, c.passes, true, s);
+    cudaError_t e;
+    if (carried) {
+        e = tc ? la::launch_tc(a, dx, dz, c.B, c.passes, true, p, s) : la::launch_simt(a, dx, dz, bh, c.passes, true, s);
         if (e != cudaSuccess) return e;
-        la::la_carry<<<dim3((unsigned)((a.state_floats + 255) / 256), bh, c.passes), 256, 0, s>>>(a, p.d_log);
+        const unsigned blocks = (unsigned)((a.state_floats / 4 + la::kCarryThreads - 1) / la::kCarryThreads);
+        la::la_carry<<<dim3(blocks, bh, c.passes), la::kCarryThreads, 0, s>>>(a, p.d_log);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return tc ? la::launch_tc_main(a, dx, dz, bh, c.passes, p, s) : la::launch_simt(a, dx, dz, bh, c.passes, false, s);
+    return tc ? la::launch_tc(a, dx, dz, c.B, c.passes, false, p, s) : la::launch_simt(a, dx, dz, bh, c.passes, false, s);
 }
 
 cudaError_t launch_la_step(const fftconv_linattn_s& p, const LaStep& c, cudaStream_t s) {

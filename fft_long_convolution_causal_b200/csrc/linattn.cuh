@@ -2,6 +2,8 @@
 // a call and the length of a row.
 #pragma once
 
+#include <atomic>
+
 #include "mixer.h"
 
 namespace fftc {
@@ -23,9 +25,23 @@ __device__ __forceinline__ int64_t live_tokens(const Args& a, int b) {
     return n < 0 ? 0 : n > a.N ? a.N : n;
 }
 
-// tcgen05 kernels (bf16): the segments' own states, and the outputs.
-cudaError_t launch_tc_states(const Args& a, int dx, int dz, int bh, int passes, const fftconv_linattn_s& p, cudaStream_t s);
-cudaError_t launch_tc_main(const Args& a, int dx, int dz, int bh, int passes, const fftconv_linattn_s& p, cudaStream_t s);
+// The shared-memory limit of a kernel, set once a device (again at worst).
+template <auto kKernel>
+cudaError_t allow(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load() & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done |= bit;
+    return e;
+}
+
+// tcgen05 kernels (bf16): the segments' own states of the passes that carry them, or the outputs.
+cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool states, const fftconv_linattn_s& p,
+                      cudaStream_t s);
 
 }  // namespace la
 }  // namespace fftc
