@@ -3,11 +3,16 @@
 //
 // la_main: a CTA walks the chunks of one (segment, row, head, pass) with the
 // state S [dx][dz] resident in tensor memory.  Per chunk of L live tokens:
-//   scores  P  = X Y^T                                   (128 x 128 x DX)
-//   inter   OI = X bf16(S)                               (128 x DZ x DX)
-//   intra   OA = bf16(s_p a^|i-j| P, masked) Z           (128 x DZ x 128)
-//   out     o  = OA + s_i a^(i+1) OI                     (rows of bf16)
-//   state   S  = a^L S + (s_u a^(L-1-j) y_j)^T Z         (DX x DZ x 128, two products)
+//   scores  P = X Y^T                                    (128 x 128 x DX)
+//   inter   O = X bf16(S), its rows times s_i a^(i+1)    (128 x DZ x DX)
+//   intra   O += bf16(s_p a^|i-j| P, masked) Z           (128 x DZ x 128)
+//   state   S = a^L S + (s_u a^(L-1-j) y_j)^T Z          (DX x DZ x 128, two products)
+// Eight warps turn scores into P' and then split y; four do the state's decay and
+// bf16 copy, the scaling of O's rows and the outputs.  One warp issues products,
+// in the order inter, intra, state, next scores, so that a chunk's scores are
+// weighed and its y split while the state and the next copies are under way; one
+// warp issues copies.  Probing a barrier costs about 100 cycles and handing over
+// through one 116, so each step waits for one barrier that several arrive at.
 // The decayed y would lose bits in one bf16, and with it the state that all later
 // outputs read: it is split into a sum of two (off by 2^-17 at most).
 //
@@ -58,6 +63,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int sr
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;\n" ::: "memory");
 }
+// (x, y) times (a, b), two products an instruction
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+    asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -72,6 +83,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c
         "[%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(mbar)
         : "memory");
+}
+// a block of a tile out to global memory; rows and elements out of range are not written
+__device__ __forceinline__ void tma_store_4d(const void* map, uint32_t src, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
 }
 // byte offset of 16-byte column c of token t in a tile (128-byte swizzle: column xor row)
 __device__ __forceinline__ uint32_t tile_off(int t, int c) {
@@ -90,12 +108,15 @@ struct Source {
     CUtensorMap map;
     int at_token, at_head, at_row;  // dimension 1 .. 3 of each, 0: not a dimension (stride zero or one element)
     int by_hand;                    // no map: copied with plain loads
+    __device__ __forceinline__ int at(int dim, int t, int h, int b) const {
+        return at_token == dim ? t : at_head == dim ? h : at_row == dim ? b : 0;
+    }
 };
-constexpr int kMaxSources = 4;
+constexpr int kMaxSources = 4 + kLaMaxPasses;
 struct Args {
     la::Args a;
     Source src[kMaxSources];
-    int x[kLaMaxPasses], y[kLaMaxPasses], z[kLaMaxPasses];  // sources of each pass
+    int x[kLaMaxPasses], y[kLaMaxPasses], z[kLaMaxPasses], out[kLaMaxPasses];  // maps of each pass
     int* err;
     uint32_t limit;
 };
@@ -107,10 +128,12 @@ struct Waiter {
     __device__ __forceinline__ bool operator()(const uint64_t& x, uint32_t parity) const {
         const uint32_t ad = smem_u32(&x);
 #pragma unroll 1
-        for (uint32_t i = 0; i < limit && !*abort; ++i)
-            if (um::mbar_try_wait(ad, parity)) return true;
-        *abort = 1;
-        return false;
+        for (uint32_t i = 0; !um::mbar_try_wait(ad, parity); ++i)
+            if (*abort || i >= limit) {
+                *abort = 1;
+                return false;
+            }
+        return true;
     }
     // one answer for a warp
     __device__ __forceinline__ bool all(const uint64_t& x, uint32_t parity) const {
@@ -142,67 +165,59 @@ struct Span {
     __device__ __forceinline__ int tokens(int n) const { return (int)min((int64_t)kC, live - start(n)); }
 };
 
-// One warp copies the tiles of every chunk into a ring: y, x, z (or y, z) by turns.
-template <int DX, int DZ, int kItems, int kSlots, uint32_t kSlot>
-__device__ __forceinline__ void copy_tiles(const Args& g, const LaPass& p, const Span& sp, int b, int h, uint32_t ring,
-                                           uint64_t* full, uint64_t* empty, const Waiter& wait) {
-    const int lane = threadIdx.x & 31, pass = blockIdx.z;
-    int made = 0;
-    bool ok = true;
-#pragma unroll 1
-    for (int n = 0; n < sp.nch && ok; ++n) {
+// The copying warp's view: which tile is copied where.
+struct Copier {
+    const Args& g;
+    const LaPass& p;
+    const Span& sp;
+    int b, h;
+    const Waiter& wait;
+    // Tile `what` (0 y, 1 x, 2 z) of chunk n to dst, the use-th copy there, once the one before was left; false: a wait
+    // gave up.
+    __device__ __forceinline__ bool operator()(int what, int blocks, int n, uint32_t dst, const uint64_t& full,
+                                               const uint64_t& empty, int use) const {
+        const int lane = threadIdx.x & 31, pass = blockIdx.z;
+        if (use > 0 && !wait.all(empty, (uint32_t)(use - 1) & 1u)) return false;
         const int64_t t0 = sp.start(n);
         const int L = sp.tokens(n);
+        const Source& src = g.src[what == 2 ? g.z[pass] : what == 1 ? g.x[pass] : g.y[pass]];
+        const uint32_t bar = smem_u32(&full);
+        if (src.by_hand || (L < kC && sp.first + t0 + L < g.a.N)) {
+            // rows behind the length are zeros whatever memory holds
+            const fftconv_strides& st = what == 2 ? p.sz : what == 1 ? p.sx : p.sy;
+            const __nv_bfloat16* base = (const __nv_bfloat16*)(what == 2 ? p.z : what == 1 ? p.x : p.y) + b * st.batch +
+                                        h * st.head + (sp.first + t0) * st.token;
+            const int d = what == 2 ? p.dz : p.dx;
 #pragma unroll 1
-        for (int it = 0; it < kItems; ++it, ++made) {
-            const bool is_z = it == kItems - 1;
-            const Source& s = g.src[is_z ? g.z[pass] : it == 0 ? g.y[pass] : g.x[pass]];
-            const int sl = made % kSlots, blocks = (is_z ? DZ : DX) / 64;
-            const uint32_t dst = ring + (uint32_t)sl * kSlot, bar = smem_u32(&full[sl]);
-            if (made >= kSlots && !wait.all(empty[sl], (uint32_t)(made / kSlots - 1) & 1u)) {
-                ok = false;
-                break;
+            for (int e = lane; e < kC * blocks * 8; e += 32) {
+                const int c = e % (blocks * 8), t = e / (blocks * 8);
+                const bool on = t < L && c * 8 < d;
+                cp_async16(dst + tile_off(t, c), on ? base + t * st.token + c * 8 : base, on ? 16 : 0);
             }
-            if (s.by_hand || (L < kC && sp.first + t0 + L < g.a.N)) {
-                // rows behind the length are zeros whatever memory holds
-                const fftconv_strides& st = is_z ? p.sz : it == 0 ? p.sy : p.sx;
-                const __nv_bfloat16* base = (const __nv_bfloat16*)(is_z ? p.z : it == 0 ? p.y : p.x) + b * st.batch +
-                                            h * st.head + (sp.first + t0) * st.token;
-                const int d = is_z ? p.dz : p.dx;
-#pragma unroll 1
-                for (int e = lane; e < kC * blocks * 8; e += 32) {
-                    const int c = e % (blocks * 8), t = e / (blocks * 8);
-                    const bool on = t < L && c * 8 < d;
-                    cp_async16(dst + tile_off(t, c), on ? base + t * st.token + c * 8 : base, on ? 16 : 0);
-                }
-                cp_wait();
-                um::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) um::mbar_arrive(bar);
-            } else if (lane == 0) {
-                const int t = (int)(sp.first + t0);
-                auto at = [&](int dim) { return s.at_token == dim ? t : s.at_head == dim ? h : s.at_row == dim ? b : 0; };
-                um::mbar_arrive_expect_tx(bar, (uint32_t)blocks * kBlock);
-#pragma unroll 1
-                for (int k = 0; k < blocks; ++k)
-                    tma_load_4d(dst + (uint32_t)k * kBlock, &s.map, 64 * k, at(1), at(2), at(3), bar);
-            }
+            cp_wait();
+            um::fence_proxy_async();
             __syncwarp();
-        }
-    }
-    // copies still in flight after a wait gave up land before the CTA ends
-    if (!ok || *wait.abort) {
+            if (lane == 0) um::mbar_arrive(bar);
+        } else if (lane == 0) {
+            const int t = (int)(sp.first + t0);
+            const int c1 = src.at(1, t, h, b), c2 = src.at(2, t, h, b), c3 = src.at(3, t, h, b);
+            um::mbar_arrive_expect_tx(bar, (uint32_t)blocks * kBlock);
 #pragma unroll 1
-        for (int i = made > kSlots ? made - kSlots : 0; i < made; ++i)
-            um::mbar_wait(smem_u32(&full[i % kSlots]), (uint32_t)(i / kSlots) & 1u);
+            for (int k = 0; k < blocks; ++k)
+                tma_load_4d(dst + (uint32_t)k * kBlock, &src.map, 64 * k, c1, c2, c3, bar);
+        }
+        __syncwarp();
+        return true;
     }
-}
+};
+// Probes for a copy in flight when a wait elsewhere gave up: it lands before the CTA ends.
+constexpr uint32_t kLanding = 64;
 
 // y decayed to the chunk's end, as a sum of NS bf16 terms: the first in place, the others `lo` apart.
 // Thread (token t, part q of Q) takes every Q-th 16-byte column.
 template <int DX, int NS, int Q>
 __device__ __forceinline__ void split_y(uint32_t tile, uint32_t lo, uint32_t lo_step, int t, int q, float w) {
-#pragma unroll 2
+#pragma unroll 4
     for (int c = q; c < DX / 8; c += Q) {
         const uint32_t off = tile_off(t, c);
         const uint4 u = lds128(tile + off);
@@ -210,12 +225,12 @@ __device__ __forceinline__ void split_y(uint32_t tile, uint32_t lo, uint32_t lo_
         uint32_t o[NS][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float x = w * lo_f(in[i]), y = w * hi_f(in[i]);
+            float x = lo_f(in[i]), y = hi_f(in[i]);
+            mul2(x, y, w, w);
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 o[s][i] = pack2(x, y);
-                x -= lo_f(o[s][i]);
-                y -= hi_f(o[s][i]);
+                x -= lo_f(o[s][i]), y -= hi_f(o[s][i]);
             }
         }
         sts128(tile + off, o[0][0], o[0][1], o[0][2], o[0][3]);
@@ -224,9 +239,19 @@ __device__ __forceinline__ void split_y(uint32_t tile, uint32_t lo, uint32_t lo_
     }
 }
 
+// One thread of a converged warp.  The issuing warp runs its loop as a whole, so that descriptors stay in uniform
+// registers, and only the products themselves are elected: issued from a branch on the lane, each product of
+// 64 cycles took 99.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 // Every product issued is complete before tensor memory is freed.
 __device__ __forceinline__ void drain(uint64_t& bar, volatile int* abort) {
-    um::mma_commit(smem_u32(&bar));
+    if (elect()) um::mma_commit(smem_u32(&bar));
+    __syncwarp();
     if (!um::mbar_wait(smem_u32(&bar), 0)) *abort = 1;
 }
 
@@ -234,25 +259,25 @@ __device__ __forceinline__ void drain(uint64_t& bar, volatile int* abort) {
 template <int DX, int DZ>
 struct Main {
     static constexpr bool kTwo = DX == 64 && DZ == 64;  // two CTAs an SM
-    static constexpr uint32_t kSlot = (uint32_t)(DX > DZ ? DX : DZ) * 256u;
-    static constexpr uint32_t kS = (uint32_t)DX * DZ * 2u, kLo = (uint32_t)DX * 256u;
-    static constexpr int kSlots = 5;
+    static constexpr uint32_t kTX = (uint32_t)DX * 256u, kTZ = (uint32_t)DZ * 256u;  // bytes of a tile
+    static constexpr uint32_t kS = (uint32_t)DX * DZ * 2u, kLo = kTX;
+    // Tiles: two of y, one of x, two of z.  x is done with after inter, y after the state's product, z after the
+    // output staged in it has left: the next x, the next z and the y after next are requested in that order.
+    static constexpr int kTiles = 5;
     // The state's product has 128 rows whatever DX is: with DX = 64 its descriptor reads 16 KiB behind
     // a term of y (rows nobody looks at), which has to be this CTA's memory.
-    static constexpr uint32_t kOffLo = kSlots * kSlot, kOffS = kOffLo + kLo, kOffTail = kOffS + kS;
+    static constexpr uint32_t kOffLo = 3 * kTX + 2 * kTZ, kOffS = kOffLo + kLo, kOffTail = kOffS + kS;
     static constexpr uint32_t kTail = DX == 64 && kS < 16384u ? 16384u - kS : 2048u;
     static constexpr uint32_t kBytes = kOffTail + kTail;
-    // tensor-memory columns
-    static constexpr uint32_t kP = 0;                     // scores, then P' in the first 64
-    static constexpr uint32_t kOA = DZ == 64 ? 64 : 128;  // DZ = 64: the scores' upper half, free by then
-    static constexpr uint32_t kOI = DZ == 64 ? 128 : 256;
-    static constexpr uint32_t kST = DZ == 64 ? 192 : 384;
-    static constexpr uint32_t kCols = DZ == 64 ? 256 : 512;
+    // tensor-memory columns: scores, O, the state.  P' (bf16) replaces the first quarter of each half of the scores:
+    // the two warps of a row each overwrite only what they have read.
+    static constexpr uint32_t kP = 0, kO = 128, kST = kO + DZ, kCols = DZ == 64 ? 256 : 512;
     static constexpr int kThreads = 3 * 128 + 64;
 };
 struct MainTail {
-    uint64_t full[5], empty[5], pfull, pready, ofull, ofree, sfull, yfull, sdone, drain;
-    float pw[kLaPowers], ct[32], dt[64];
+    uint64_t xy[2], zfull[2], empty[5], pfull, pored, iready, ifull, ofull, staged, yfull, sdone, drain;
+    alignas(16) float ct[32];  // read four at a time
+    float pw[kLaPowers], dt[64];
     uint32_t tmem;
     int abort;
 };
@@ -261,7 +286,7 @@ template <int DX, int DZ>
 __global__ void __launch_bounds__((Main<DX, DZ>::kThreads), (Main<DX, DZ>::kTwo ? 2 : 1))
 la_main(const __grid_constant__ Args g) {
     using K = Main<DX, DZ>;
-    static_assert(sizeof(MainTail) <= K::kTail, "the tail holds the barriers and tables");
+    static_assert(sizeof(MainTail) <= K::kTail && K::kOffTail % 16 == 0, "the tail holds the barriers and tables");
     extern __shared__ __align__(1024) uint8_t smem[];
     MainTail& m = *reinterpret_cast<MainTail*>(smem + K::kOffTail);
     const la::Args& a = g.a;
@@ -276,19 +301,21 @@ la_main(const __grid_constant__ Args g) {
     constexpr int kMmaWarp = 12, kCopyWarp = 13;
 
     if (tid == 0) {
-        for (int i = 0; i < K::kSlots; ++i) {
-            um::mbar_init(smem_u32(&m.full[i]), 1);
-            um::mbar_init(smem_u32(&m.empty[i]), 1);
+        for (int i = 0; i < 2; ++i) {
+            um::mbar_init(smem_u32(&m.xy[i]), 2);
+            um::mbar_init(smem_u32(&m.zfull[i]), 1);
         }
+        for (int i = 0; i < K::kTiles; ++i) um::mbar_init(smem_u32(&m.empty[i]), 1);
         um::mbar_init(smem_u32(&m.pfull), 1);
-        um::mbar_init(smem_u32(&m.pready), 4);
+        um::mbar_init(smem_u32(&m.pored), 12);  // P' in place, O's rows scaled
+        um::mbar_init(smem_u32(&m.iready), 4);  // the state decayed and copied, O read
+        um::mbar_init(smem_u32(&m.ifull), 1);
         um::mbar_init(smem_u32(&m.ofull), 1);
-        um::mbar_init(smem_u32(&m.ofree), 4);
-        um::mbar_init(smem_u32(&m.sfull), 4);
-        um::mbar_init(smem_u32(&m.yfull), 4);
+        um::mbar_init(smem_u32(&m.staged), 4);
+        um::mbar_init(smem_u32(&m.yfull), 8);
         um::mbar_init(smem_u32(&m.sdone), 1);
         um::mbar_init(smem_u32(&m.drain), 1);
-        m.abort = 0;
+        m.abort = g.limit == 0;  // no wait at all: the first that would gives up
     }
     const float* pow_h = a.pw + (size_t)h * kLaPowers;
     for (int i = tid; i < kLaPowers; i += K::kThreads) m.pw[i] = pow_h[i];
@@ -305,76 +332,100 @@ la_main(const __grid_constant__ Args g) {
     const uint32_t tmem = m.tmem;
     const int quarter = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
-    auto slot = [](int n, int item) { return (3 * n + item) % K::kSlots; };
-    auto phase = [](int n, int item) { return (uint32_t)((3 * n + item) / K::kSlots) & 1u; };
-    auto tile = [&](int n, int item) { return sb + (uint32_t)slot(n, item) * K::kSlot; };
+    // tile `item` (0 y, 1 x, 2 z) of chunk n: its place, how often that was used before, and where it is
+    auto slot = [](int n, int item) { return item == 1 ? 2 : item == 0 ? n & 1 : 3 + (n & 1); };
+    auto use = [](int n, int item) { return item == 1 ? n : n >> 1; };
+    auto tile = [&](int n, int item) {
+        return sb + (item == 1 ? 2 * K::kTX : item == 0 ? (uint32_t)(n & 1) * K::kTX : 3 * K::kTX + (uint32_t)(n & 1) * K::kTZ);
+    };
 
     if (warp == kMmaWarp) {
-        if (lane == 0) {
-            constexpr uint32_t id_scores = um::idesc_bf16(128, 128), id_inter = um::idesc_bf16(128, DZ) | um::kBmn,
-                               id_state = id_inter | um::kAmn;
-            const uint64_t ds = um::sdesc(sb + K::kOffS, 128, DX * 16);
+        constexpr uint32_t id_scores = um::idesc_bf16(128, 128), id_inter = um::idesc_bf16(128, DZ) | um::kBmn,
+                           id_state = id_inter | um::kAmn;
+        const uint64_t ds = um::sdesc(sb + K::kOffS, 128, DX * 16), kx = kmajor(tile(0, 1)), yl = mnmajor(sb + K::kOffLo);
+        // chunk n of the walk, -1: the first chunk's scores
 #pragma unroll 1
-            for (int n = 0; n < nch; ++n) {
-                const uint32_t par = (uint32_t)n & 1u, prev = par ^ 1u;
-                const uint64_t ky = kmajor(tile(n, 0)), kx = kmajor(tile(n, 1)), zz = mnmajor(tile(n, 2));
-                if (!wait(m.full[slot(n, 0)], phase(n, 0))) break;
-                if (!wait(m.full[slot(n, 1)], phase(n, 1))) break;
-                if (DZ == 64 && n && !wait(m.ofree, prev)) break;
+        for (int n = -1; n < nch; ++n) {
+            const uint32_t par = (uint32_t)n & 1u, half = (uint32_t)(n >> 1) & 1u;
+            if (n >= 0) {
+                const uint64_t zz = mnmajor(tile(n, 2)), yh = mnmajor(tile(n, 0));
+                if (!wait.all(m.iready, par)) break;
                 um::fence_after();
+                if (elect()) {
 #pragma unroll
-                for (int k = 0; k < DX / 16; ++k)
-                    um::mma_ss(tmem + K::kP, kx + kstep(k), ky + kstep(k), id_scores, k > 0);
-                um::mma_commit(smem_u32(&m.pfull));
-                if (!wait(m.sfull, par)) break;
-                if (DZ != 64 && n && !wait(m.ofree, prev)) break;
+                    for (int k = 0; k < DX / 16; ++k)
+                        um::mma_ss(tmem + K::kO, kx + kstep(k), ds + (uint64_t)(k * 16), id_inter, k > 0);
+                    um::mma_commit(smem_u32(&m.ifull));
+                    um::mma_commit(smem_u32(&m.empty[2]));
+                }
+                __syncwarp();
+                if (!wait.all(m.zfull[n & 1], half) || !wait.all(m.pored, par)) break;
                 um::fence_after();
+                if (elect()) {
 #pragma unroll
-                for (int k = 0; k < DX / 16; ++k)
-                    um::mma_ss(tmem + K::kOI, kx + kstep(k), ds + (uint64_t)(k * 16), id_inter, k > 0);
-                um::mma_commit(smem_u32(&m.empty[slot(n, 1)]));
-                if (!wait(m.full[slot(n, 2)], phase(n, 2))) break;
-                if (!wait(m.pready, par)) break;
-                um::fence_after();
+                    for (int k = 0; k < kC / 16; ++k)
+                        um::mma_ts(tmem + K::kO, tmem + K::kP + (k / 4) * 64u + (k % 4) * 8u, zz + mnstep(k), id_inter, 1);
+                    um::mma_commit(smem_u32(&m.ofull));
+                }
+                __syncwarp();
+                if (n + 1 < nch) {  // nobody reads the state behind the last chunk
+                    if (!wait.all(m.yfull, par)) break;
+                    um::fence_after();
+                    if (elect()) {
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k)
-                    um::mma_ts(tmem + K::kOA, tmem + K::kP + 8u * k, zz + mnstep(k), id_inter, k > 0);
-                um::mma_commit(smem_u32(&m.ofull));
-                if (!wait(m.yfull, par)) break;
-                um::fence_after();
-                const uint64_t yh = mnmajor(tile(n, 0)), yl = mnmajor(sb + K::kOffLo);
+                        for (int k = 0; k < kC / 16; ++k)
+                            um::mma_ss(tmem + K::kST, yl + mnstep(k), zz + mnstep(k), id_state, 1);
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k) um::mma_ss(tmem + K::kST, yl + mnstep(k), zz + mnstep(k), id_state, 1);
-#pragma unroll
-                for (int k = 0; k < kC / 16; ++k) um::mma_ss(tmem + K::kST, yh + mnstep(k), zz + mnstep(k), id_state, 1);
-                um::mma_commit(smem_u32(&m.sdone));
-                um::mma_commit(smem_u32(&m.empty[slot(n, 0)]));
-                um::mma_commit(smem_u32(&m.empty[slot(n, 2)]));
+                        for (int k = 0; k < kC / 16; ++k)
+                            um::mma_ss(tmem + K::kST, yh + mnstep(k), zz + mnstep(k), id_state, 1);
+                        um::mma_commit(smem_u32(&m.sdone));
+                        um::mma_commit(smem_u32(&m.empty[n & 1]));
+                    }
+                    __syncwarp();
+                }
             }
-            drain(m.drain, &m.abort);
+            if (n + 1 < nch) {
+                const int c = n + 1;
+                const uint64_t ky = kmajor(tile(c, 0));
+                if (!wait.all(m.xy[c & 1], (uint32_t)(c >> 1) & 1u)) break;
+                um::fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int k = 0; k < DX / 16; ++k)
+                        um::mma_ss(tmem + K::kP, kx + kstep(k), ky + kstep(k), id_scores, k > 0);
+                    um::mma_commit(smem_u32(&m.pfull));
+                }
+                __syncwarp();
+            }
         }
-        __syncwarp();
+        drain(m.drain, &m.abort);
     } else if (warp == kCopyWarp) {
-        copy_tiles<DX, DZ, 3, K::kSlots, K::kSlot>(g, p, sp, b, h, sb, m.full, m.empty, wait);
-    } else if (warp >= 8) {
-        // ================================================ the split of y
-        const int t = 32 * quarter + lane;
+        const Copier copy{g, p, sp, b, h, wait};
+        auto load = [&](int n, int item) {
+            return n >= nch || copy(item, (item == 2 ? DZ : DX) / 64, n, tile(n, item), item == 2 ? m.zfull[n & 1] : m.xy[n & 1],
+                                    m.empty[slot(n, item)], use(n, item));
+        };
+        // y0 x0 z0 y1, then x, z of chunk n and y of chunk n + 1
+        bool ok = load(0, 0);
+        int i = 0;
 #pragma unroll 1
-        for (int n = 0; n < nch; ++n) {
-            const int L = sp.tokens(n);
-            const float w = p.s_u * (rev ? m.pw[t + 1] : m.pw[max(L - 1 - t, 0)]);
-            if (!wait.all(m.full[slot(n, 0)], phase(n, 0))) break;
-            if (!wait.all(m.pfull, (uint32_t)n & 1u)) break;                  // the scores have read y
-            if (n && !wait.all(m.sdone, (uint32_t)(n - 1) & 1u)) break;       // the state has read the other term
-            split_y<DX, 2, 1>(tile(n, 0), sb + K::kOffLo, 0, t, 0, w);
-            um::fence_proxy_async();
-            arrive(m.yfull);
+        for (; i < 3 * nch && ok; ++i) {
+            const int n = i / 3, it = i % 3;
+            ok = load(it == 2 ? n + 1 : n, it == 2 ? 0 : it + 1);
         }
-    } else if (warp >= 4) {
-        // ================================================ the state's decay and its bf16 copy
+        if (!ok || *wait.abort) {  // the last two chunks' copies may be in flight
+            const int n = i / 3;
+            for (int c = n > 1 ? n - 1 : 0; c <= n && c < nch; ++c) {
+                um::mbar_wait(smem_u32(&m.zfull[c & 1]), (uint32_t)(c >> 1) & 1u, kLanding);
+                um::mbar_wait(smem_u32(&m.xy[c & 1]), (uint32_t)(c >> 1) & 1u, kLanding);
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ================================================ the state's decay and bf16 copy, O's rows, outputs
         const int d = 32 * quarter + lane;
         const bool mine = 32 * quarter < DX;  // this warp's lanes hold rows of the state
         const uint32_t ts = tl + K::kST;
+        const Source& so = g.src[g.out[blockIdx.z]];
         const float* s0 = p.carried ? a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats
                           : p.s_in    ? p.s_in + (size_t)bh * p.dx * p.dz
                                       : nullptr;
@@ -400,53 +451,103 @@ la_main(const __grid_constant__ Args g) {
             }
             um::wait_st();
         }
+        uint32_t o[DZ / 2];  // a row of O in bf16
+        // through z's tile (all products have read it), then out as a bulk copy
+        auto stage = [&](int n) {
+            const uint32_t tz = tile(n, 2);
+#pragma unroll
+            for (int c = 0; c < DZ / 8; ++c) sts128(tz + tile_off(d, c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            um::fence_proxy_async();
+            arrive(m.staged);
+            if (warp == 4) {
+                if (!wait.all(m.staged, (uint32_t)n & 1u)) return;
+                if (lane == 0) {
+                    const int tk = (int)(sp.first + sp.start(n));
+                    const int c1 = so.at(1, tk, h, b), c2 = so.at(2, tk, h, b), c3 = so.at(3, tk, h, b);
 #pragma unroll 1
-        for (int n = 0; n < nch; ++n) {
-            const float f = m.pw[sp.tokens(n)];
-            if (n && !wait.all(m.sdone, (uint32_t)(n - 1) & 1u)) break;
-            um::fence_after();
+                    for (int k = 0; k < DZ / 64; ++k)
+                        if (64 * k < p.dz) tma_store_4d(&so.map, tz + (uint32_t)k * kBlock, 64 * k, c1, c2, c3);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+                __syncwarp();
+            }
+        };
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; n < nch && ok; ++n) {
+            const int L = sp.tokens(n);
+            const float f = m.pw[L];
             if (mine) {
                 const uint32_t dst = sb + K::kOffS + (uint32_t)d * 16u;
 #pragma unroll 1
-                for (int n0 = 0; n0 < DZ; n0 += 32) {
-                    uint32_t r[32];
-                    um::ld32x32_x32(ts + n0, r);
-                    um::wait_ld<32>(r);
+                for (int n0 = 0; n0 < DZ; n0 += 16) {
+                    uint32_t r[16];
+                    um::ld32x32_x16(ts + n0, r);
+                    um::wait_ld<16>(r);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 2; ++q)
                         sts128(dst + (uint32_t)(n0 / 8 + q) * (DX * 16u), pack2(as_f(r[8 * q]), as_f(r[8 * q + 1])),
                                pack2(as_f(r[8 * q + 2]), as_f(r[8 * q + 3])), pack2(as_f(r[8 * q + 4]), as_f(r[8 * q + 5])),
                                pack2(as_f(r[8 * q + 6]), as_f(r[8 * q + 7])));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = as_u(f * as_f(r[i]));
+                    for (int i = 0; i < 16; ++i) r[i] = as_u(f * as_f(r[i]));
                     um::st32x32_x16(ts + n0, r);
-                    um::st32x32_x16(ts + n0 + 16, r + 16);
                 }
                 um::wait_st();
             }
             um::fence_proxy_async();
-            arrive(m.sfull);
-        }
-    } else {
-        // ================================================ scores -> P', outputs
-        const int i = 32 * quarter + lane;
-        __nv_bfloat16* out = (__nv_bfloat16*)p.out + b * p.so.batch + h * p.so.head + sp.first * p.so.token;
-        const bool wide = ((reinterpret_cast<uintptr_t>(p.out) & 31u) == 0) &&
-                          ((p.so.batch | p.so.head | p.so.token) % 16 == 0);
-        const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-        const float* diag = m.dt + 31 - lane;
-#pragma unroll 1
-        for (int n = 0; n < nch; ++n) {
-            const uint32_t par = (uint32_t)n & 1u;
-            const int L = sp.tokens(n);
-            if (!wait.all(m.pfull, par)) break;
+            arrive(m.iready);
+            if (n) stage(n - 1);
+            const float fo = p.s_i * (rev ? m.pw[max(L - 1 - d, 0)] : m.pw[d + 1]);
+            if (!(ok = wait.all(m.ifull, (uint32_t)n & 1u))) break;
             um::fence_after();
 #pragma unroll 1
-            for (int jb = 0; jb < 4; ++jb) {
+            for (int n0 = 0; n0 < DZ; n0 += 16) {
+                uint32_t r[16];
+                um::ld32x32_x16(tl + K::kO + n0, r);
+                um::wait_ld<16>(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = as_u(fo * as_f(r[i]));
+                um::st32x32_x16(tl + K::kO + n0, r);
+            }
+            um::wait_st();
+            arrive(m.pored);
+            if (n && warp == 4 && lane == 0) {  // the last chunk's outputs have left z's tile
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                um::mbar_arrive(smem_u32(&m.empty[3 + ((n - 1) & 1)]));
+            }
+            if (!(ok = wait.all(m.ofull, (uint32_t)n & 1u))) break;
+            um::fence_after();
+#pragma unroll
+            for (int n0 = 0; n0 < DZ; n0 += 16) {
+                uint32_t r[16];
+                um::ld32x32_x16(tl + K::kO + n0, r);
+                um::wait_ld<16>(r);
+                // rows behind the length are zeros
+#pragma unroll
+                for (int c = 0; c < 8; ++c) o[n0 / 2 + c] = d < L ? pack2(as_f(r[2 * c]), as_f(r[2 * c + 1])) : 0u;
+            }
+            if (n + 1 < nch) ok = wait.all(m.sdone, (uint32_t)n & 1u);
+            um::fence_after();
+        }
+        if (ok && nch) stage(nch - 1);
+        if (warp == 4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    } else {
+        // ================================================ scores -> P', and the split of y
+        const int i = 32 * quarter + lane, part = warp >> 3;  // row (then token), half of its columns
+        const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+        const float* diag = m.dt + 31 - lane;
+        const uint32_t tp = tl + K::kP;
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n) {
+            if (!wait.all(m.pfull, (uint32_t)n & 1u)) break;
+            um::fence_after();
+#pragma unroll 1
+            for (int jb = 2 * part; jb < 2 * part + 2; ++jb) {
                 uint32_t o[16];
                 if (rev ? jb >= quarter : jb <= quarter) {
                     uint32_t r[32];
-                    um::ld32x32_x32(tl + K::kP + 32u * jb, r);
+                    um::ld32x32_x32(tp + 32u * jb, r);
                     um::wait_ld<32>(r);
                     if (jb == quarter) {
 #pragma unroll
@@ -457,10 +558,13 @@ la_main(const __grid_constant__ Args g) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 k = *reinterpret_cast<const float4*>(m.ct + c);
-                            r[c] = as_u(as_f(r[c]) * (f * k.x));
-                            r[c + 1] = as_u(as_f(r[c + 1]) * (f * k.y));
-                            r[c + 2] = as_u(as_f(r[c + 2]) * (f * k.z));
-                            r[c + 3] = as_u(as_f(r[c + 3]) * (f * k.w));
+                            float x[4] = {as_f(r[c]), as_f(r[c + 1]), as_f(r[c + 2]), as_f(r[c + 3])};
+                            mul2(x[0], x[1], k.x, k.y);
+                            mul2(x[2], x[3], k.z, k.w);
+                            mul2(x[0], x[1], f, f);
+                            mul2(x[2], x[3], f, f);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) r[c + e] = as_u(x[e]);
                         }
                     }
 #pragma unroll
@@ -469,41 +573,26 @@ la_main(const __grid_constant__ Args g) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c) o[c] = 0u;
                 }
-                um::st32x32_x16(tl + K::kP + 16u * jb, o);
+                um::st32x32_x16(tp + 64u * part + 16u * (jb & 1), o);
             }
             um::wait_st();
-            arrive(m.pready);
-            const float f = p.s_i * (rev ? m.pw[max(L - 1 - i, 0)] : m.pw[i + 1]);
-            __nv_bfloat16* row = out + (sp.start(n) + i) * p.so.token;
-            if (!wait.all(m.ofull, par)) break;
-            um::fence_after();
-#pragma unroll 1
-            for (int n0 = 0; n0 < DZ; n0 += 16) {
-                uint32_t ra[16], ri[16], o[8];
-                um::ld32x32_x16(tl + K::kOA + n0, ra);
-                um::ld32x32_x16(tl + K::kOI + n0, ri);
-                um::wait_ld<16>(ra);
-                um::wait_ld<16>(ri);
-                if (n0 + 16 >= DZ) arrive(m.ofree);
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    o[c] = pack2(fmaf(f, as_f(ri[2 * c]), as_f(ra[2 * c])), fmaf(f, as_f(ri[2 * c + 1]), as_f(ra[2 * c + 1])));
-                if (i < L) {
-                    if (wide && n0 + 16 <= p.dz) {
-                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(row + n0), "r"(o[0]),
-                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                     : "memory");
-                    } else {
-                        if (n0 < p.dz) *reinterpret_cast<uint4*>(row + n0) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (n0 + 8 < p.dz) *reinterpret_cast<uint4*>(row + n0 + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                }
+            arrive(m.pored);
+            if (n + 1 < nch) {
+                // the scores have read y, and all products before them the other term
+                const int L = sp.tokens(n);
+                split_y<DX, 2, 2>(tile(n, 0), sb + K::kOffLo, 0, i, part, p.s_u * (rev ? m.pw[i + 1] : m.pw[max(L - 1 - i, 0)]));
+                um::fence_proxy_async();
+                arrive(m.yfull);
             }
         }
-        // rows behind the sequence
-        for (int64_t e = tid; e < (sp.rows - sp.live) * (p.dz / 8); e += 128)
-            *reinterpret_cast<uint4*>(out + (sp.live + e / (p.dz / 8)) * p.so.token + 8 * (e % (p.dz / 8))) =
-                make_uint4(0u, 0u, 0u, 0u);
+        // chunks behind the sequence
+        const int64_t from = (int64_t)nch * kC;
+        if (from < sp.rows) {
+            __nv_bfloat16* out = (__nv_bfloat16*)p.out + b * p.so.batch + h * p.so.head + (sp.first + from) * p.so.token;
+            for (int64_t r = 16 * part + i / 8; r < sp.rows - from; r += 32)
+                for (int c = i % 8; c < p.dz / 8; c += 8)
+                    *reinterpret_cast<uint4*>(out + r * p.so.token + 8 * c) = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     um::fence_before();
     __syncthreads();
@@ -563,7 +652,7 @@ la_states(const __grid_constant__ Args g) {
             um::mbar_init(smem_u32(&m.ufree[i]), 4);
         }
         um::mbar_init(smem_u32(&m.drain), 1);
-        m.abort = 0;
+        m.abort = g.limit == 0;  // no wait at all: the first that would gives up
     }
     for (int i = tid; i < kLaPowers; i += K::kThreads) m.pw[i] = a.pw[(size_t)h * kLaPowers + i];
     if (warp == kMmaWarp) {
@@ -580,17 +669,17 @@ la_states(const __grid_constant__ Args g) {
     auto tile = [&](int n, int item) { return sb + (uint32_t)slot(n, item) * K::kSlot; };
 
     if (warp == kMmaWarp) {
-        if (lane == 0) {
-            constexpr uint32_t id = um::idesc_bf16(128, DZ) | um::kAmn | um::kBmn;
+        constexpr uint32_t id = um::idesc_bf16(128, DZ) | um::kAmn | um::kBmn;
 #pragma unroll 1
-            for (int n = 0; n < nch; ++n) {
-                const uint32_t u = tmem + K::kU + (uint32_t)(n & 1) * DZ;
-                const uint64_t zz = mnmajor(tile(n, 1)), yh = mnmajor(tile(n, 0)), y1 = mnmajor(sb + K::kOffLo),
-                               y2 = mnmajor(sb + K::kOffLo + K::kLo);
-                if (!wait(m.full[slot(n, 1)], phase(n, 1))) break;
-                if (n > 1 && !wait(m.ufree[n & 1], (uint32_t)(n / 2 - 1) & 1u)) break;
-                if (!wait(m.yfull, (uint32_t)n & 1u)) break;
-                um::fence_after();
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t u = tmem + K::kU + (uint32_t)(n & 1) * DZ;
+            const uint64_t zz = mnmajor(tile(n, 1)), yh = mnmajor(tile(n, 0)), y1 = mnmajor(sb + K::kOffLo),
+                           y2 = mnmajor(sb + K::kOffLo + K::kLo);
+            if (!wait.all(m.full[slot(n, 1)], phase(n, 1))) break;
+            if (n > 1 && !wait.all(m.ufree[n & 1], (uint32_t)(n / 2 - 1) & 1u)) break;
+            if (!wait.all(m.yfull, (uint32_t)n & 1u)) break;
+            um::fence_after();
+            if (elect()) {
                 // the smallest terms first: fewer truncations next to a large sum
 #pragma unroll
                 for (int k = 0; k < kC / 16; ++k) um::mma_ss(u, y2 + mnstep(k), zz + mnstep(k), id, k > 0);
@@ -603,11 +692,20 @@ la_states(const __grid_constant__ Args g) {
                 um::mma_commit(smem_u32(&m.empty[slot(n, 0)]));
                 um::mma_commit(smem_u32(&m.empty[slot(n, 1)]));
             }
-            drain(m.drain, &m.abort);
+            __syncwarp();
         }
-        __syncwarp();
+        drain(m.drain, &m.abort);
     } else if (warp == kCopyWarp) {
-        copy_tiles<DX, DZ, 2, K::kSlots, K::kSlot>(g, p, sp, b, h, sb, m.full, m.empty, wait);
+        const Copier copy{g, p, sp, b, h, wait};
+        int made = 0;
+#pragma unroll 1
+        for (; made < 2 * nch; ++made) {
+            const int n = made >> 1, it = made & 1, s = made % K::kSlots;
+            if (!copy(2 * it, (it ? DZ : DX) / 64, n, tile(n, it), m.full[s], m.empty[s], made / K::kSlots)) break;
+        }
+        if (*wait.abort)
+            for (int j = made > K::kSlots ? made - K::kSlots : 0; j < made; ++j)
+                um::mbar_wait(smem_u32(&m.full[j % K::kSlots]), (uint32_t)(j / K::kSlots) & 1u, kLanding);
     } else if (warp >= 4) {
         // ================================================ the split of y: 8 warps
         const int t = 32 * quarter + lane, q = (warp - 4) / 4;
@@ -787,6 +885,10 @@ cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool sta
         g.x[i] = source(q.x, q.sx, q.dx);
         g.y[i] = source(q.y, q.sy, q.dx);
         g.z[i] = source(q.z, q.sz, q.dz);
+        if (!states) {
+            g.out[i] = source(q.out, q.so, q.dz);
+            if (g.src[g.out[i]].by_hand) return cudaErrorInvalidValue;
+        }
     }
     const int bh = B * a.H;
     if (dx <= 64)
