@@ -8,7 +8,7 @@
 //   dq = pass(do, v, k) forward, dk = pass(v, do, q) and dv = pass(k, q, do) in reverse.
 // Every exponent is >= 0, so nothing overflows however strong the decay is.
 //
-// bf16 runs on the tensor cores (linattn_tc.cu), fp32 here.  The token axis is cut into segments where one CTA per (row, head) would leave
+// bf16 runs on tcgen05 (linattn_tc.cu), fp32 here.  The token axis is cut into segments where one CTA per (row, head) would leave
 // SMs idle: a first kernel sums each segment's own contribution to the state, a
 // second carries the states over the segments, the third computes the outputs.
 #include <cuda_bf16.h>
@@ -24,37 +24,104 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
+// ---- fp32 on the tensor cores: every operand as a sum of two tf32 values (the
+// second exact to 2^-23 of the first's), three products, the largest last.  The
+// product of the two small parts, below 2^-24, is left out.
+struct Two {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Two split(float x) {
+    Two r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r.hi) : "f"(x));
+    r.lo = __float_as_uint(x - __uint_as_float(r.hi));
+    return r;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Adds the products of one A and N B fragments (those of `mask`) to acc.  Summed from zero and added in fp32: the
+// tensor core truncates when it accumulates, and over the dozens of steps of a sum that bias reached 4e-6.
+template <int N>
+__device__ __forceinline__ void mma3(float (&acc)[N][4], const Two (&a)[4], const Two (&b)[N][2], uint32_t mask = ~0u) {
+    float u[N][4];
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[q][e] = 0.f;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        if (mask >> q & 1u) mma_tf32(u[q], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[q][0].hi, b[q][1].hi);
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        if (mask >> q & 1u) mma_tf32(u[q], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[q][0].lo, b[q][1].lo);
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        if (mask >> q & 1u) mma_tf32(u[q], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[q][0].hi, b[q][1].hi);
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[q][e] += u[q][e];
+}
+// fragments of rows i0.., columns k0.. of a row-major matrix (A), and of its transpose (B: columns are rows)
+template <int P>
+__device__ __forceinline__ void frag_a(Two (&a)[4], const float* m, int i0, int k0, int g, int t) {
+    const float* p = m + (i0 + g) * P + k0 + t;
+    a[0] = split(p[0]), a[1] = split(p[8 * P]), a[2] = split(p[4]), a[3] = split(p[8 * P + 4]);
+}
+template <int P>
+__device__ __forceinline__ void frag_bt(Two (&b)[2], const float* m, int n0, int k0, int g, int t) {
+    const float* p = m + (n0 + g) * P + k0 + t;
+    b[0] = split(p[0]), b[1] = split(p[4]);
+}
+template <int P>
+__device__ __forceinline__ void frag_b(Two (&b)[2], const float* m, int k0, int n0, int g, int t) {
+    const float* p = m + (k0 + t) * P + n0 + g;
+    b[0] = split(p[0]), b[1] = split(p[4 * P]);
+}
+
+// Row pitches (floats): 4 or 8 more than a multiple of 32, so that the 8 rows x 4 columns (or 4 x 8) of a
+// fragment lie in 32 different banks.
 template <int DX, int DZ>
 struct Shape {
-    static constexpr int PX = DX + 4, PZ = DZ + 4, PP = kC + 4;  // row pitches (floats)
-    static constexpr int kFloats = 2 * kC * PX + kC * PZ + kC * PP + DX * PZ + 132;
+    static constexpr int PX = DX + 4, PZ = DZ + 8, PP = kC + 4;
+    static constexpr int kFloats = 2 * kC * PX + kC * PZ + kC * PP + DX * PZ + kLaPowers;
+    static constexpr int kCtas = DX == 64 && DZ == 64 ? 2 : 1;
 };
 
-// rows [t0, t0 + kC) of a tensor into shared memory as fp32, zeros behind row `live` and column d
+// rows of a tensor into shared memory, zeros behind row `live` and column d
 template <int D, int P>
 __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t stride, int live, int d) {
     for (int e = threadIdx.x; e < kC * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = 4 * (e % (D / 4));
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < live && c < d) v = load4(src + r * stride + c);
-        *reinterpret_cast<float4*>(dst + r * P + c) = v;
+        const bool on = r < live && c < d;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(dst + r * P + c)),
+                     "l"(on ? src + r * stride + c : src), "r"(on ? 16 : 0)
+                     : "memory");
     }
 }
 
-// grid (segments, rows x heads, passes); STATES: only the segments' own states
+// grid (segments, rows x heads, passes); STATES: only the segments' own states.
+// Warp w has rows 16 (w & 3) of scores and outputs, and half w >> 2 of their
+// columns; the state lives in registers as accumulators (m-tiles w & 3, + 4),
+// with a copy in shared memory for the outputs.
 template <int DX, int DZ, bool STATES>
-__global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, (Shape<DX, DZ>::kCtas)) la_f32(const __grid_constant__ Args a) {
     using S = Shape<DX, DZ>;
+    constexpr int MT = DX / 64, NT = DZ / 16;  // state tiles of a warp: MT x NT of 16 x 8
     extern __shared__ __align__(16) float sm[];
     float *xs = sm, *ys = xs + kC * S::PX, *zs = ys + kC * S::PX, *ps = zs + kC * S::PZ, *ss = ps + kC * S::PP,
           *pw = ss + DX * S::PZ;
     const LaPass& p = a.p[blockIdx.z];
     const int tid = threadIdx.x, sg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
-    const int ti = tid / 16, tj = tid % 16;
+    const int lane = tid & 31, g = lane >> 2, t = lane & 3, warp = tid >> 5, mi = warp & 3, nj = warp >> 2;
+    const bool rev = p.reverse;
     const int64_t first = sg * a.seg, len = live_tokens(a, b);
     const int64_t rows = min(a.seg, a.N - first);                   // output rows of this segment
     const int64_t live = max((int64_t)0, min(rows, len - first));   // of which read
@@ -65,118 +132,145 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
     float* wseg = a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats;
     for (int i = tid; i < kLaPowers; i += kThreads) pw[i] = a.pw[h * kLaPowers + i];
     // the state entering the segment
+    if (STATES)
+        let_next_start();
+    else
+        after_previous();
     const float* s0 = STATES ? nullptr : p.carried ? wseg : p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
     const bool trans = !p.carried && p.in_trans;
-    for (int e = tid; e < DX * DZ; e += kThreads) {
-        const int d = e / DZ, n = e % DZ;
-        ss[d * S::PZ + n] = s0 && d < p.dx && n < p.dz ? s0[trans ? n * p.dx + d : d * p.dz + n] : 0.f;
-    }
+    float st[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = 16 * (mi + 4 * m) + g + 8 * (e >> 1), n = 8 * (nj * NT + q) + 2 * t + (e & 1);
+                st[m][q][e] = s0 && d < p.dx && n < p.dz ? s0[trans ? n * p.dx + d : d * p.dz + n] : 0.f;
+            }
     const int nch = (int)((live + kC - 1) / kC);
+#pragma unroll 1
     for (int ch = 0; ch < nch; ++ch) {
-        const int64_t t0 = (int64_t)(p.reverse ? nch - 1 - ch : ch) * kC;
+        const int64_t t0 = (int64_t)(rev ? nch - 1 - ch : ch) * kC;
         const int L = (int)min((int64_t)kC, live - t0);
         __syncthreads();
         if (!STATES) load_tile<DX, S::PX>(xs, x + t0 * p.sx.token, p.sx.token, L, p.dx);
         load_tile<DX, S::PX>(ys, y + t0 * p.sy.token, p.sy.token, L, p.dx);
         load_tile<DZ, S::PZ>(zs, z + t0 * p.sz.token, p.sz.token, L, p.dz);
+        if (!STATES) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int q = 0; q < NT; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2)
+                        *reinterpret_cast<float2*>(ss + (16 * (mi + 4 * m) + g + 4 * e) * S::PZ + 8 * (nj * NT + q) + 2 * t) =
+                            make_float2(st[m][q][e], st[m][q][e + 1]);
+        }
+        asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;\n" ::: "memory");
         __syncthreads();
         if (!STATES) {
-            float acc[4][4] = {};
-            for (int d = 0; d < DX; d += 4) {
-                float4 u[4], v[4];
+            // scores: 16 x 32 a warp, 8-column tiles on the far side of the diagonal left out
+            {
+                float acc[4][4] = {};
+                uint32_t near = 0;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    u[r] = *reinterpret_cast<float4*>(xs + (ti + 16 * r) * S::PX + d);
-                    v[r] = *reinterpret_cast<float4*>(ys + (tj + 16 * r) * S::PX + d);
-                }
+                for (int q = 0; q < 4; ++q)
+                    near |= (rev ? 32 * nj + 8 * q + 7 >= 16 * mi : 32 * nj + 8 * q <= 16 * mi + 15) ? 1u << q : 0u;
+                if (near)
+#pragma unroll 2
+                    for (int k = 0; k < DX; k += 8) {
+                        Two fa[4], fb[4][2];
+                        frag_a<S::PX>(fa, xs, 16 * mi, k, g, t);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[r][c] += u[r].x * v[c].x + u[r].y * v[c].y + u[r].z * v[c].z + u[r].w * v[c].w;
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int i = ti + 16 * r, j = tj + 16 * c, e = p.reverse ? j - i : i - j;
-                    ps[i * S::PP + j] = e >= 0 ? p.s_p * pw[e] * acc[r][c] : 0.f;
-                }
-            __syncthreads();
-#pragma unroll
-            for (int m = 0; m < DZ / 64; ++m) {
-                const int n = 4 * tj + 64 * m;
-                float4 o[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int d = 0; d < DX; d += 4) {
-                    float4 sv[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) sv[q] = *reinterpret_cast<float4*>(ss + (d + q) * S::PZ + n);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float4 u = *reinterpret_cast<float4*>(xs + (ti + 16 * r) * S::PX + d);
-                        o[r].x += u.x * sv[0].x + u.y * sv[1].x + u.z * sv[2].x + u.w * sv[3].x;
-                        o[r].y += u.x * sv[0].y + u.y * sv[1].y + u.z * sv[2].y + u.w * sv[3].y;
-                        o[r].z += u.x * sv[0].z + u.y * sv[1].z + u.z * sv[2].z + u.w * sv[3].z;
-                        o[r].w += u.x * sv[0].w + u.y * sv[1].w + u.z * sv[2].w + u.w * sv[3].w;
+                        for (int q = 0; q < 4; ++q) frag_bt<S::PX>(fb[q], ys, 32 * nj + 8 * q, k, g, t);
+                        mma3(acc, fa, fb, near);
                     }
-                }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = ti + 16 * r;
-                    const float f = p.s_i * (p.reverse ? pw[max(L - 1 - i, 0)] : pw[i + 1]);
-                    o[r].x *= f, o[r].y *= f, o[r].z *= f, o[r].w *= f;
-                }
-                for (int j = 0; j < kC; j += 4) {
-                    float4 zv[4];
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) zv[q] = *reinterpret_cast<float4*>(zs + (j + q) * S::PZ + n);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float4 u = *reinterpret_cast<float4*>(ps + (ti + 16 * r) * S::PP + j);
-                        o[r].x += u.x * zv[0].x + u.y * zv[1].x + u.z * zv[2].x + u.w * zv[3].x;
-                        o[r].y += u.x * zv[0].y + u.y * zv[1].y + u.z * zv[2].y + u.w * zv[3].y;
-                        o[r].z += u.x * zv[0].z + u.y * zv[1].z + u.z * zv[2].z + u.w * zv[3].z;
-                        o[r].w += u.x * zv[0].w + u.y * zv[1].w + u.z * zv[2].w + u.w * zv[3].w;
+                    for (int r = 0; r < 2; ++r) {
+                        const int i = 16 * mi + g + 8 * r, j = 32 * nj + 8 * q + 2 * t, e = rev ? j - i : i - j;
+                        const float u = e >= 0 ? p.s_p * pw[e] * acc[q][2 * r] : 0.f;
+                        const int f = rev ? e + 1 : e - 1;
+                        const float v = f >= 0 ? p.s_p * pw[f] * acc[q][2 * r + 1] : 0.f;
+                        *reinterpret_cast<float2*>(ps + i * S::PP + j) = make_float2(u, v);
                     }
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = ti + 16 * r;
-                    if (i < L && n < p.dz) store4(out + (t0 + i) * p.so.token + n, o[r]);
-                }
             }
             __syncthreads();
+            // outputs: 16 x DZ / 2 a warp
+            float acc[NT][4] = {};
+#pragma unroll 2
+            for (int k = 0; k < DX; k += 8) {
+                Two fa[4], fb[NT][2];
+                frag_a<S::PX>(fa, xs, 16 * mi, k, g, t);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], ss, k, 8 * (nj * NT + q), g, t);
+                mma3(acc, fa, fb);
+            }
+            const int i0 = 16 * mi + g;
+            const float f0 = p.s_i * (rev ? pw[max(L - 1 - i0, 0)] : pw[i0 + 1]),
+                        f1 = p.s_i * (rev ? pw[max(L - 9 - i0, 0)] : pw[i0 + 9]);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) acc[q][0] *= f0, acc[q][1] *= f0, acc[q][2] *= f1, acc[q][3] *= f1;
+            const int from = rev ? 16 * mi : 0, to = rev ? kC : 16 * mi + 16;
+#pragma unroll 2
+            for (int k = from; k < to; k += 8) {
+                Two fa[4], fb[NT][2];
+                frag_a<S::PP>(fa, ps, 16 * mi, k, g, t);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], zs, k, 8 * (nj * NT + q), g, t);
+                mma3(acc, fa, fb);
+            }
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = i0 + 8 * r, n = 8 * (nj * NT + q) + 2 * t;
+                    if (i < L && n < p.dz)
+                        *reinterpret_cast<float2*>(out + (t0 + i) * p.so.token + n) =
+                            make_float2(acc[q][2 * r], acc[q][2 * r + 1]);
+                }
         }
-        // S <- a^L S + s_u sum_j a^(..) y_j^T z_j
-        const float fl = pw[L];
+        if (STATES || ch + 1 < nch || (!p.carried && p.s_out)) {
+            // S <- a^L S + s_u sum_j a^(..) y_j^T z_j
+            const float fl = pw[L];
 #pragma unroll
-        for (int m = 0; m < DZ / 64; ++m) {
-            const int n = 4 * tj + 64 * m;
-            float4 acc[DX / 16];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int r = 0; r < DX / 16; ++r) {
-                acc[r] = *reinterpret_cast<float4*>(ss + (ti + 16 * r) * S::PZ + n);
-                acc[r].x *= fl, acc[r].y *= fl, acc[r].z *= fl, acc[r].w *= fl;
-            }
-            for (int j = 0; j < L; ++j) {
-                const float w = p.s_u * pw[p.reverse ? j + 1 : L - 1 - j];
-                const float4 zv = *reinterpret_cast<float4*>(zs + j * S::PZ + n);
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
-                for (int r = 0; r < DX / 16; ++r) {
-                    const float u = w * ys[j * S::PX + ti + 16 * r];
-                    acc[r].x += u * zv.x, acc[r].y += u * zv.y, acc[r].z += u * zv.z, acc[r].w += u * zv.w;
+                    for (int e = 0; e < 4; ++e) st[m][q][e] *= fl;
+#pragma unroll 1
+            for (int k = 0; k < L; k += 8) {
+                const float w0 = p.s_u * pw[rev ? k + t + 1 : max(L - 1 - k - t, 0)],
+                            w1 = p.s_u * pw[rev ? k + t + 5 : max(L - 5 - k - t, 0)];
+                Two fb[NT][2];
+#pragma unroll
+                for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], zs, k, 8 * (nj * NT + q), g, t);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const float* v = ys + (k + t) * S::PX + 16 * (mi + 4 * m) + g;
+                    Two fa[4];
+                    fa[0] = split(w0 * v[0]), fa[1] = split(w0 * v[8]);
+                    fa[2] = split(w1 * v[4 * S::PX]), fa[3] = split(w1 * v[4 * S::PX + 8]);
+                    mma3(st[m], fa, fb);
                 }
             }
-#pragma unroll
-            for (int r = 0; r < DX / 16; ++r) *reinterpret_cast<float4*>(ss + (ti + 16 * r) * S::PZ + n) = acc[r];
         }
     }
-    __syncthreads();
     float* so = STATES ? wseg : !p.carried && p.s_out ? p.s_out + (size_t)bh * p.dx * p.dz : nullptr;
     if (so)
-        for (int e = tid; e < p.dx * p.dz; e += kThreads) so[e] = ss[(e / p.dz) * S::PZ + e % p.dz];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int d = 16 * (mi + 4 * m) + g + 4 * e, n = 8 * (nj * NT + q) + 2 * t;
+                    if (d < p.dx && n < p.dz)
+                        *reinterpret_cast<float2*>(so + (size_t)d * p.dz + n) = make_float2(st[m][q][e], st[m][q][e + 1]);
+                }
     if (!STATES)  // rows behind the sequence
         for (int64_t e = tid; e < (rows - live) * (p.dz / 4); e += kThreads)
             store4(out + (live + e / (p.dz / 4)) * p.so.token + 4 * (e % (p.dz / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
@@ -188,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) la_simt(const __grid_constant__ Args
 constexpr int kCarryThreads = 128;
 __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant__ Args a, const double* __restrict__ lg) {
     const LaPass& p = a.p[blockIdx.z];
-    if (!p.carried) return;
+    let_next_start();
     __shared__ float decay[kLaMaxSegments];  // over a segment; below zero: an empty one
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, n = p.dx * p.dz;
     const int64_t len = live_tokens(a, b);
@@ -199,6 +293,7 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
         decay[k] = live > 0 ? (float)exp(lg[h] * (double)live) : -1.f;
     }
     __syncthreads();
+    after_previous();
     const int e = 4 * (blockIdx.x * kCarryThreads + threadIdx.x);
     if (e >= n) return;
     float* w = a.work + blockIdx.z * a.pass_floats + (size_t)bh * a.nseg * a.state_floats + e;
@@ -236,17 +331,14 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
 template <int DX, int DZ>
 cudaError_t run(const Args& a, int bh, int passes, bool states, cudaStream_t s) {
     constexpr int bytes = Shape<DX, DZ>::kFloats * (int)sizeof(float);
-    const cudaError_t e = states ? allow<la_simt<DX, DZ, true>>(bytes) : allow<la_simt<DX, DZ, false>>(bytes);
+    const cudaError_t e = states ? allow<la_f32<DX, DZ, true>>(bytes) : allow<la_f32<DX, DZ, false>>(bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid(a.nseg, bh, passes);
-    if (states)
-        la_simt<DX, DZ, true><<<grid, kThreads, bytes, s>>>(a);
-    else
-        la_simt<DX, DZ, false><<<grid, kThreads, bytes, s>>>(a);
-    return cudaGetLastError();
+    return states ? launch<la_f32<DX, DZ, true>>(grid, kThreads, bytes, s, false, a)
+                  : launch<la_f32<DX, DZ, false>>(grid, kThreads, bytes, s, a.nseg > 1, a);
 }
 
-cudaError_t launch_simt(const Args& a, int dx, int dz, int bh, int passes, bool states, cudaStream_t s) {
+cudaError_t launch_f32(const Args& a, int dx, int dz, int bh, int passes, bool states, cudaStream_t s) {
     if (dx <= 64)
         return dz <= 64 ? run<64, 64>(a, bh, passes, states, s) : run<64, 128>(a, bh, passes, states, s);
     return dz <= 64 ? run<128, 64>(a, bh, passes, states, s) : run<128, 128>(a, bh, passes, states, s);
@@ -376,11 +468,11 @@ int segments(const fftconv_linattn_s& p, int B, int64_t N, int passes) {
 }  // namespace
 
 size_t la_workspace_floats(const fftconv_linattn_s& p, int passes) {
-    // enough for every B and N up to the plan's: one state a CTA, and the bound on segments times CTAs
-    const int64_t chunks = (p.N + chunk_of(p) - 1) / chunk_of(p), ctas = (int64_t)p.B * p.H * passes;
-    const int64_t most = ctas * (chunks < kLaMaxSegments ? chunks : kLaMaxSegments), cap = kLaMaxWaves * slots_of(p, passes);
-    const int64_t states = most < cap ? most : cap > ctas ? cap : ctas;
-    return (size_t)states * p.dk * p.dv;
+    // enough for every B and N up to the plan's: segments times CTAs is bounded above, one segment needs none
+    const int64_t chunks = (p.N + chunk_of(p) - 1) / chunk_of(p), cap = kLaMaxWaves * slots_of(p, passes);
+    if (chunks == 1) return 0;
+    const int64_t most = (int64_t)p.B * p.H * passes * (chunks < kLaMaxSegments ? chunks : kLaMaxSegments);
+    return (size_t)(most < cap ? most : cap) * p.dk * p.dv;
 }
 
 cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t s) {
@@ -396,26 +488,28 @@ cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t 
     a.work = c.work;
     a.state_floats = (size_t)p.dk * p.dv;
     a.pass_floats = (size_t)c.B * p.H * a.nseg * a.state_floats;
-    bool carried = false;
+    bool ends = false;
     for (int i = 0; i < c.passes; ++i) {
         a.p[i] = c.pass[i];
-        // the tensor-core outputs' kernel keeps its state for the outputs alone: states that a caller
-        // asks for come from the states' kernel, which sums them in fp32
-        a.p[i].carried = a.nseg > 1 || (tc && a.p[i].s_out);
-        carried = carried || a.p[i].carried;
+        a.p[i].carried = a.nseg > 1;
+        ends = ends || a.p[i].s_out;
     }
     int dx, dz;
     padded(p, c.passes, &dx, &dz);
     const int bh = c.B * p.H;
     cudaError_t e;
-    if (carried) {
-        e = tc ? la::launch_tc(a, dx, dz, c.B, c.passes, true, p, s) : la::launch_simt(a, dx, dz, bh, c.passes, true, s);
+    if (a.nseg > 1) {
+        e = tc ? la::launch_tc(a, dx, dz, c.B, c.passes, true, p, s) : la::launch_f32(a, dx, dz, bh, c.passes, true, s);
         if (e != cudaSuccess) return e;
         const unsigned blocks = (unsigned)((a.state_floats / 4 + la::kCarryThreads - 1) / la::kCarryThreads);
-        la::la_carry<<<dim3(blocks, bh, c.passes), la::kCarryThreads, 0, s>>>(a, p.d_log);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = la::launch<la::la_carry>(dim3(blocks, bh, c.passes), la::kCarryThreads, 0, s, true, a, p.d_log);
+        if (e != cudaSuccess) return e;
     }
-    return tc ? la::launch_tc(a, dx, dz, c.B, c.passes, false, p, s) : la::launch_simt(a, dx, dz, bh, c.passes, false, s);
+    e = tc ? la::launch_tc(a, dx, dz, c.B, c.passes, false, p, s) : la::launch_f32(a, dx, dz, bh, c.passes, false, s);
+    // The tensor-core outputs' kernel keeps its state for the outputs alone: final states that a caller asks for come
+    // from the states' kernel, which sums them in fp32 (after the outputs: a caller may update its states in place).
+    if (e == cudaSuccess && tc && a.nseg == 1 && ends) e = la::launch_tc(a, dx, dz, c.B, c.passes, true, p, s);
+    return e;
 }
 
 cudaError_t launch_la_step(const fftconv_linattn_s& p, const LaStep& c, cudaStream_t s) {

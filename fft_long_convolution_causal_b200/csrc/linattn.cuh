@@ -39,6 +39,27 @@ cudaError_t allow(int bytes) {
     return e;
 }
 
+// Launches that may begin while the kernel before them in the stream still runs (`early`): it calls let_next_start,
+// they call after_previous before they touch what it writes.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <auto kKernel, typename... A>
+cudaError_t launch(dim3 grid, int threads, size_t bytes, cudaStream_t s, bool early, const A&... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = bytes;
+    c.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &attr;
+    c.numAttrs = early ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kKernel, args...);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 // tcgen05 kernels (bf16): the segments' own states of the passes that carry them, or the outputs.
 cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool states, const fftconv_linattn_s& p,
                       cudaStream_t s);

@@ -248,6 +248,26 @@ __device__ __forceinline__ bool elect() {
     return r != 0;
 }
 
+// 32 columns of row d of a state (zero: none) into tensor memory, all loads in flight together; trans: stored [dz][dx]
+__device__ __forceinline__ void state_in(uint32_t ts, const float* s0, bool trans, const LaPass& p, int d, int n0) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 && d < p.dx && n0 + i < p.dz) {
+            if (trans) {
+                const float* q = s0 + (size_t)(n0 + i) * p.dx + d;
+                v = make_float4(q[0], q[p.dx], q[2 * p.dx], q[3 * p.dx]);
+            } else {
+                v = *reinterpret_cast<const float4*>(s0 + (size_t)d * p.dz + n0 + i);
+            }
+        }
+        r[i] = as_u(v.x), r[i + 1] = as_u(v.y), r[i + 2] = as_u(v.z), r[i + 3] = as_u(v.w);
+    }
+    um::st32x32_x16(ts + n0, r);
+    um::st32x32_x16(ts + n0 + 16, r + 16);
+}
+
 // Every product issued is complete before tensor memory is freed.
 __device__ __forceinline__ void drain(uint64_t& bar, volatile int* abort) {
     if (elect()) um::mma_commit(smem_u32(&bar));
@@ -299,8 +319,24 @@ la_main(const __grid_constant__ Args g) {
     const uint32_t sb = smem_u32(smem);
     const Waiter wait{&m.abort, g.limit};
     constexpr int kMmaWarp = 12, kCopyWarp = 13;
+    // tile `item` (0 y, 1 x, 2 z) of chunk n: its place, how often that was used before, and where it is
+    auto slot = [](int n, int item) { return item == 1 ? 2 : item == 0 ? n & 1 : 3 + (n & 1); };
+    auto use = [](int n, int item) { return item == 1 ? n : n >> 1; };
+    auto tile = [&](int n, int item) {
+        return sb + (item == 1 ? 2 * K::kTX : item == 0 ? (uint32_t)(n & 1) * K::kTX : 3 * K::kTX + (uint32_t)(n & 1) * K::kTZ);
+    };
+    const Copier copy{g, p, sp, b, h, wait};
+    auto load = [&](int n, int item) {
+        return n >= nch || copy(item, (item == 2 ? DZ : DX) / 64, n, tile(n, item), item == 2 ? m.zfull[n & 1] : m.xy[n & 1],
+                                m.empty[slot(n, item)], use(n, item));
+    };
+    // the order of the copies: y0, then x, z of chunk n and y of chunk n + 1
+    auto load_next = [&](int i) {
+        const int k = i ? (i - 1) / 3 : -1, r = i ? (i - 1) % 3 : 2;
+        return r == 2 ? load(k + 1, 0) : load(k, r + 1);
+    };
 
-    if (tid == 0) {
+    if (tid == 32 * kCopyWarp) {
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(smem_u32(&m.xy[i]), 2);
             um::mbar_init(smem_u32(&m.zfull[i]), 1);
@@ -317,6 +353,12 @@ la_main(const __grid_constant__ Args g) {
         um::mbar_init(smem_u32(&m.drain), 1);
         m.abort = g.limit == 0;  // no wait at all: the first that would gives up
     }
+    constexpr int kFirst = 4;  // the first copies need not wait for the other warps
+    if (warp == kCopyWarp) {
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < kFirst; ++i) load_next(i);
+    }
     const float* pow_h = a.pw + (size_t)h * kLaPowers;
     for (int i = tid; i < kLaPowers; i += K::kThreads) m.pw[i] = pow_h[i];
     // weights on the diagonal block by column - row + 31, and on the others by column
@@ -332,13 +374,6 @@ la_main(const __grid_constant__ Args g) {
     const uint32_t tmem = m.tmem;
     const int quarter = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
-    // tile `item` (0 y, 1 x, 2 z) of chunk n: its place, how often that was used before, and where it is
-    auto slot = [](int n, int item) { return item == 1 ? 2 : item == 0 ? n & 1 : 3 + (n & 1); };
-    auto use = [](int n, int item) { return item == 1 ? n : n >> 1; };
-    auto tile = [&](int n, int item) {
-        return sb + (item == 1 ? 2 * K::kTX : item == 0 ? (uint32_t)(n & 1) * K::kTX : 3 * K::kTX + (uint32_t)(n & 1) * K::kTZ);
-    };
-
     if (warp == kMmaWarp) {
         constexpr uint32_t id_scores = um::idesc_bf16(128, 128), id_inter = um::idesc_bf16(128, DZ) | um::kBmn,
                            id_state = id_inter | um::kAmn;
@@ -400,21 +435,12 @@ la_main(const __grid_constant__ Args g) {
         }
         drain(m.drain, &m.abort);
     } else if (warp == kCopyWarp) {
-        const Copier copy{g, p, sp, b, h, wait};
-        auto load = [&](int n, int item) {
-            return n >= nch || copy(item, (item == 2 ? DZ : DX) / 64, n, tile(n, item), item == 2 ? m.zfull[n & 1] : m.xy[n & 1],
-                                    m.empty[slot(n, item)], use(n, item));
-        };
-        // y0 x0 z0 y1, then x, z of chunk n and y of chunk n + 1
-        bool ok = load(0, 0);
-        int i = 0;
+        bool ok = !*wait.abort;
+        int i = kFirst;
 #pragma unroll 1
-        for (; i < 3 * nch && ok; ++i) {
-            const int n = i / 3, it = i % 3;
-            ok = load(it == 2 ? n + 1 : n, it == 2 ? 0 : it + 1);
-        }
+        for (; i <= 3 * nch && ok; ++i) ok = load_next(i);
         if (!ok || *wait.abort) {  // the last two chunks' copies may be in flight
-            const int n = i / 3;
+            const int n = (i + 2) / 3;
             for (int c = n > 1 ? n - 1 : 0; c <= n && c < nch; ++c) {
                 um::mbar_wait(smem_u32(&m.zfull[c & 1]), (uint32_t)(c >> 1) & 1u, kLanding);
                 um::mbar_wait(smem_u32(&m.xy[c & 1]), (uint32_t)(c >> 1) & 1u, kLanding);
@@ -429,26 +455,10 @@ la_main(const __grid_constant__ Args g) {
         const float* s0 = p.carried ? a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats
                           : p.s_in    ? p.s_in + (size_t)bh * p.dx * p.dz
                                       : nullptr;
-        const bool trans = !p.carried && p.in_trans, on = s0 && d < p.dx;
+        la::after_previous();  // the states entering the segments
         if (mine) {
 #pragma unroll 1
-            for (int n0 = 0; n0 < DZ; n0 += 16) {
-                uint32_t r[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (on && n0 + i < p.dz) {
-                        if (trans) {
-                            const float* q = s0 + (size_t)(n0 + i) * p.dx + d;
-                            v = make_float4(q[0], q[p.dx], q[2 * p.dx], q[3 * p.dx]);
-                        } else {
-                            v = *reinterpret_cast<const float4*>(s0 + (size_t)d * p.dz + n0 + i);
-                        }
-                    }
-                    r[i] = as_u(v.x), r[i + 1] = as_u(v.y), r[i + 2] = as_u(v.z), r[i + 3] = as_u(v.w);
-                }
-                um::st32x32_x16(ts + n0, r);
-            }
+            for (int n0 = 0; n0 < DZ; n0 += 32) state_in(ts, s0, !p.carried && p.in_trans, p, d, n0);
             um::wait_st();
         }
         uint32_t o[DZ / 2];  // a row of O in bf16
@@ -616,7 +626,7 @@ struct States {
     static constexpr int kThreads = 3 * 128 + 64;
 };
 struct StatesTail {
-    uint64_t full[5], empty[5], yfull, lofree, ufull[2], ufree[2], drain;
+    uint64_t full[5], empty[5], yfull[2], lofree[2], ufull[2], ufree[2], drain;
     float pw[kLaPowers];
     uint32_t tmem;
     int abort;
@@ -631,7 +641,7 @@ la_states(const __grid_constant__ Args g) {
     StatesTail& m = *reinterpret_cast<StatesTail*>(smem + K::kOffTail);
     const la::Args& a = g.a;
     const LaPass& p = a.p[blockIdx.z];
-    if (!p.carried) return;
+    if (!p.carried && !p.s_out) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
     const Span sp(a, p, sg, b);
@@ -645,9 +655,9 @@ la_states(const __grid_constant__ Args g) {
             um::mbar_init(smem_u32(&m.full[i]), 1);
             um::mbar_init(smem_u32(&m.empty[i]), 1);
         }
-        um::mbar_init(smem_u32(&m.yfull), 8);
-        um::mbar_init(smem_u32(&m.lofree), 1);
         for (int i = 0; i < 2; ++i) {
+            um::mbar_init(smem_u32(&m.yfull[i]), 8);
+            um::mbar_init(smem_u32(&m.lofree[i]), 1);
             um::mbar_init(smem_u32(&m.ufull[i]), 1);
             um::mbar_init(smem_u32(&m.ufree[i]), 4);
         }
@@ -662,6 +672,7 @@ la_states(const __grid_constant__ Args g) {
     um::fence_before();
     __syncthreads();
     um::fence_after();
+    la::let_next_start();
     const uint32_t tmem = m.tmem;
     const int quarter = warp & 3;
     auto slot = [](int n, int item) { return (2 * n + item) % K::kSlots; };
@@ -677,22 +688,32 @@ la_states(const __grid_constant__ Args g) {
                            y2 = mnmajor(sb + K::kOffLo + K::kLo);
             if (!wait.all(m.full[slot(n, 1)], phase(n, 1))) break;
             if (n > 1 && !wait.all(m.ufree[n & 1], (uint32_t)(n / 2 - 1) & 1u)) break;
-            if (!wait.all(m.yfull, (uint32_t)n & 1u)) break;
-            um::fence_after();
-            if (elect()) {
-                // the smallest terms first: fewer truncations next to a large sum
+            // half a chunk at a time, while the other half is split
+            bool ok = true;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                if (!(ok = wait.all(m.yfull[hf], (uint32_t)n & 1u))) break;
+                um::fence_after();
+                const uint64_t at = mnstep(4 * hf);
+                if (elect()) {
+                    // the smallest terms first: fewer truncations next to a large sum
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k) um::mma_ss(u, y2 + mnstep(k), zz + mnstep(k), id, k > 0);
+                    for (int k = 0; k < kC / 32; ++k)
+                        um::mma_ss(u, y2 + at + mnstep(k), zz + at + mnstep(k), id, hf > 0 || k > 0);
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k) um::mma_ss(u, y1 + mnstep(k), zz + mnstep(k), id, 1);
-                um::mma_commit(smem_u32(&m.lofree));
+                    for (int k = 0; k < kC / 32; ++k) um::mma_ss(u, y1 + at + mnstep(k), zz + at + mnstep(k), id, 1);
+                    um::mma_commit(smem_u32(&m.lofree[hf]));
 #pragma unroll
-                for (int k = 0; k < kC / 16; ++k) um::mma_ss(u, yh + mnstep(k), zz + mnstep(k), id, 1);
-                um::mma_commit(smem_u32(&m.ufull[n & 1]));
-                um::mma_commit(smem_u32(&m.empty[slot(n, 0)]));
-                um::mma_commit(smem_u32(&m.empty[slot(n, 1)]));
+                    for (int k = 0; k < kC / 32; ++k) um::mma_ss(u, yh + at + mnstep(k), zz + at + mnstep(k), id, 1);
+                    if (hf) {
+                        um::mma_commit(smem_u32(&m.ufull[n & 1]));
+                        um::mma_commit(smem_u32(&m.empty[slot(n, 0)]));
+                        um::mma_commit(smem_u32(&m.empty[slot(n, 1)]));
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
         drain(m.drain, &m.abort);
     } else if (warp == kCopyWarp) {
@@ -708,23 +729,38 @@ la_states(const __grid_constant__ Args g) {
                 um::mbar_wait(smem_u32(&m.full[j % K::kSlots]), (uint32_t)(j / K::kSlots) & 1u, kLanding);
     } else if (warp >= 4) {
         // ================================================ the split of y: 8 warps
-        const int t = 32 * quarter + lane, q = (warp - 4) / 4;
+        const int t0 = 32 * (warp & 1) + lane, q = (warp - 4) / 2;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
             const int L = sp.tokens(n);
-            const float w = p.s_u * (sp.rev ? m.pw[t + 1] : m.pw[max(L - 1 - t, 0)]);
             if (!wait.all(m.full[slot(n, 0)], phase(n, 0))) break;
-            if (n && !wait.all(m.lofree, (uint32_t)(n - 1) & 1u)) break;
-            split_y<DX, 3, 2>(tile(n, 0), sb + K::kOffLo, K::kLo, t, q, w);
-            um::fence_proxy_async();
-            arrive(m.yfull);
+            bool ok = true;
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                const int t = 64 * hf + t0;
+                const float w = p.s_u * (sp.rev ? m.pw[t + 1] : m.pw[max(L - 1 - t, 0)]);
+                if (n && !(ok = wait.all(m.lofree[hf], (uint32_t)(n - 1) & 1u))) break;
+                split_y<DX, 3, 4>(tile(n, 0), sb + K::kOffLo, K::kLo, t, q, w);
+                um::fence_proxy_async();
+                arrive(m.yfull[hf]);
+            }
+            if (!ok) break;
         }
     } else {
         // ================================================ S <- a^L S + U
         const int d = 32 * quarter + lane;
         const bool mine = 32 * quarter < DX;
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16), ts = tl + K::kST;
-        float* out = a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats + (size_t)d * p.dz;
+        const bool last = a.nseg == 1;  // the whole row: its final state, from the initial one
+        float* out = (last ? p.s_out + (size_t)bh * p.dx * p.dz
+                           : a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats) +
+                     (size_t)d * p.dz;
+        const float* s0 = last && p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
+        if (mine) {
+#pragma unroll 1
+            for (int n0 = 0; n0 < DZ; n0 += 32) state_in(ts, s0, p.in_trans, p, d, n0);
+            um::wait_st();
+        }
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
@@ -737,11 +773,11 @@ la_states(const __grid_constant__ Args g) {
                 for (int n0 = 0; n0 < DZ; n0 += 16) {
                     uint32_t u[16], s[16];
                     um::ld32x32_x16(tu + n0, u);
-                    if (n) um::ld32x32_x16(ts + n0, s);
+                    um::ld32x32_x16(ts + n0, s);
                     um::wait_ld<16>(u);
                     um::wait_ld<16>(s);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = n ? as_u(fmaf(f, as_f(s[i]), as_f(u[i]))) : u[i];
+                    for (int i = 0; i < 16; ++i) u[i] = as_u(fmaf(f, as_f(s[i]), as_f(u[i])));
                     um::st32x32_x16(ts + n0, u);
                 }
                 um::wait_st();
@@ -752,13 +788,8 @@ la_states(const __grid_constant__ Args g) {
 #pragma unroll 1
             for (int n0 = 0; n0 < DZ; n0 += 16) {
                 uint32_t r[16];
-                if (nch) {
-                    um::ld32x32_x16(ts + n0, r);
-                    um::wait_ld<16>(r);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = 0u;
-                }
+                um::ld32x32_x16(ts + n0, r);
+                um::wait_ld<16>(r);
                 if (d < p.dx) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
@@ -845,13 +876,12 @@ cudaError_t run(const Args& g, int bh, int passes, bool states, cudaStream_t s) 
     if (states) {
         using K = States<DX, DZ>;
         if ((e = la::allow<la_states<DX, DZ>>((int)K::kBytes)) != cudaSuccess) return e;
-        la_states<DX, DZ><<<grid, K::kThreads, K::kBytes, s>>>(g);
+        return la::launch<la_states<DX, DZ>>(grid, K::kThreads, K::kBytes, s, false, g);
     } else {
         using K = Main<DX, DZ>;
         if ((e = la::allow<la_main<DX, DZ>>((int)K::kBytes)) != cudaSuccess) return e;
-        la_main<DX, DZ><<<grid, K::kThreads, K::kBytes, s>>>(g);
+        return la::launch<la_main<DX, DZ>>(grid, K::kThreads, K::kBytes, s, g.a.nseg > 1, g);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace latc
