@@ -45,24 +45,31 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Adds the products of one A and N B fragments (those of `mask`) to acc.  Summed from zero and added in fp32: the
-// tensor core truncates when it accumulates, and over the dozens of steps of a sum that bias reached 4e-6.
+__device__ __forceinline__ void mma_tf32_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The products of one A and N B fragments, FIRST: into u, else added to it.  Two steps of 8 go into one u before it is
+// added to the sum in fp32: the tensor core truncates when it accumulates, and over the dozens of steps of a sum that
+// bias reached 4e-6.
+template <bool FIRST, int N>
+__device__ __forceinline__ void mma3(float (&u)[N][4], const Two (&a)[4], const Two (&b)[N][2]) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+        if (FIRST)
+            mma_tf32_zero(u[q], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[q][0].hi, b[q][1].hi);
+        else
+            mma_tf32(u[q], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[q][0].hi, b[q][1].hi);
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) mma_tf32(u[q], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[q][0].lo, b[q][1].lo);
+#pragma unroll
+    for (int q = 0; q < N; ++q) mma_tf32(u[q], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[q][0].hi, b[q][1].hi);
+}
 template <int N>
-__device__ __forceinline__ void mma3(float (&acc)[N][4], const Two (&a)[4], const Two (&b)[N][2], uint32_t mask = ~0u) {
-    float u[N][4];
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[q][e] = 0.f;
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-        if (mask >> q & 1u) mma_tf32(u[q], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[q][0].hi, b[q][1].hi);
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-        if (mask >> q & 1u) mma_tf32(u[q], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[q][0].lo, b[q][1].lo);
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-        if (mask >> q & 1u) mma_tf32(u[q], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[q][0].hi, b[q][1].hi);
+__device__ __forceinline__ void add(float (&acc)[N][4], const float (&u)[N][4]) {
 #pragma unroll
     for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -173,18 +180,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<DX, DZ>::kCtas)) la_f32(const
             // scores: 16 x 32 a warp, 8-column tiles on the far side of the diagonal left out
             {
                 float acc[4][4] = {};
-                uint32_t near = 0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    near |= (rev ? 32 * nj + 8 * q + 7 >= 16 * mi : 32 * nj + 8 * q <= 16 * mi + 15) ? 1u << q : 0u;
-                if (near)
-#pragma unroll 2
-                    for (int k = 0; k < DX; k += 8) {
+                // a warp whose columns lie on the far side of the diagonal has nothing to do
+                if (rev ? 32 * nj + 31 >= 16 * mi : 32 * nj <= 16 * mi + 15)
+#pragma unroll 1
+                    for (int k = 0; k < DX; k += 16) {
+                        float u[4][4];
                         Two fa[4], fb[4][2];
                         frag_a<S::PX>(fa, xs, 16 * mi, k, g, t);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) frag_bt<S::PX>(fb[q], ys, 32 * nj + 8 * q, k, g, t);
-                        mma3(acc, fa, fb, near);
+                        mma3<true>(u, fa, fb);
+                        frag_a<S::PX>(fa, xs, 16 * mi, k + 8, g, t);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) frag_bt<S::PX>(fb[q], ys, 32 * nj + 8 * q, k + 8, g, t);
+                        mma3<false>(u, fa, fb);
+                        add(acc, u);
                     }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -200,13 +210,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<DX, DZ>::kCtas)) la_f32(const
             __syncthreads();
             // outputs: 16 x DZ / 2 a warp
             float acc[NT][4] = {};
-#pragma unroll 2
-            for (int k = 0; k < DX; k += 8) {
+#pragma unroll 1
+            for (int k = 0; k < DX; k += 16) {
+                float u[NT][4];
                 Two fa[4], fb[NT][2];
                 frag_a<S::PX>(fa, xs, 16 * mi, k, g, t);
 #pragma unroll
                 for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], ss, k, 8 * (nj * NT + q), g, t);
-                mma3(acc, fa, fb);
+                mma3<true>(u, fa, fb);
+                frag_a<S::PX>(fa, xs, 16 * mi, k + 8, g, t);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], ss, k + 8, 8 * (nj * NT + q), g, t);
+                mma3<false>(u, fa, fb);
+                add(acc, u);
             }
             const int i0 = 16 * mi + g;
             const float f0 = p.s_i * (rev ? pw[max(L - 1 - i0, 0)] : pw[i0 + 1]),
@@ -214,13 +230,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<DX, DZ>::kCtas)) la_f32(const
 #pragma unroll
             for (int q = 0; q < NT; ++q) acc[q][0] *= f0, acc[q][1] *= f0, acc[q][2] *= f1, acc[q][3] *= f1;
             const int from = rev ? 16 * mi : 0, to = rev ? kC : 16 * mi + 16;
-#pragma unroll 2
-            for (int k = from; k < to; k += 8) {
+#pragma unroll 1
+            for (int k = from; k < to; k += 16) {
+                float u[NT][4];
                 Two fa[4], fb[NT][2];
                 frag_a<S::PP>(fa, ps, 16 * mi, k, g, t);
 #pragma unroll
                 for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], zs, k, 8 * (nj * NT + q), g, t);
-                mma3(acc, fa, fb);
+                mma3<true>(u, fa, fb);
+                frag_a<S::PP>(fa, ps, 16 * mi, k + 8, g, t);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], zs, k + 8, 8 * (nj * NT + q), g, t);
+                mma3<false>(u, fa, fb);
+                add(acc, u);
             }
 #pragma unroll
             for (int q = 0; q < NT; ++q)
@@ -243,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DX, DZ>::kCtas)) la_f32(const
                     for (int e = 0; e < 4; ++e) st[m][q][e] *= fl;
 #pragma unroll 1
             for (int k = 0; k < L; k += 8) {
+                float u[NT][4];
                 const float w0 = p.s_u * pw[rev ? k + t + 1 : max(L - 1 - k - t, 0)],
                             w1 = p.s_u * pw[rev ? k + t + 5 : max(L - 5 - k - t, 0)];
                 Two fb[NT][2];
@@ -254,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DX, DZ>::kCtas)) la_f32(const
                     Two fa[4];
                     fa[0] = split(w0 * v[0]), fa[1] = split(w0 * v[8]);
                     fa[2] = split(w1 * v[4 * S::PX]), fa[3] = split(w1 * v[4 * S::PX + 8]);
-                    mma3(st[m], fa, fb);
+                    mma3<true>(u, fa, fb);
+                    add(st[m], u);
                 }
             }
         }
