@@ -13,80 +13,69 @@
 #include <cuda_bf16.h>
 
 #include "mixer.h"
+#include "pairs.cuh"
 
 namespace fftc {
 namespace ln {
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-template <typename T, int V>
-struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Piece {
-    T e[V];
-};
-
-template <int TPR>
+// threads of a block: rows on several warps have one row a block
+template <int TPR, int N>
 __host__ __device__ constexpr int block_threads() {
-    return TPR > 32 ? TPR : 256;  // rows on several warps: one row a block
+    return TPR > 32 ? TPR : N;
 }
 
-// sums of two values over the TPR threads of a row
+// sum over the TPR threads of a row
 template <int TPR>
-__device__ __forceinline__ float2 row_sum(float2 v) {
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (TPR > 32) {
-        __shared__ float2 part[TPR / 32];
+        __shared__ float part[TPR / 32];
         __syncthreads();  // the previous sum has been read
         if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
         __syncthreads();
-        v = make_float2(0.f, 0.f);
+        v = 0.f;
 #pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) {
-            v.x += part[i].x;
-            v.y += part[i].y;
-        }
+        for (int i = 0; i < TPR / 32; ++i) v += part[i];
     }
     return v;
 }
 
 template <typename T, int V, int TPR, int E>
-__global__ void __launch_bounds__(block_threads<TPR>())
-norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias, T* y,
-         float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int C, int G, float eps) {
+__global__ void __launch_bounds__((block_threads<TPR, 256>()))
+norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias, T* y, float* __restrict__ mean,
+         float* __restrict__ rstd, int64_t rows, int C, int G, float eps) {
     using P = Piece<T, V>;
     using W = Piece<float, V>;
-    constexpr int kRows = block_threads<TPR>() / TPR;
+    constexpr int kRows = block_threads<TPR, 256>() / TPR;
     const int lane = threadIdx.x % TPR, items = C / V;
     const int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     const bool on = r < rows;
     const P* xr = reinterpret_cast<const P*>(x + (on ? r : 0) * C);
-    float v[E][V];
-    float2 s = make_float2(0.f, 0.f);
+    P p[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int c = lane + i * TPR;
-        if (c < items && on) {
-            const P p = xr[c];
-#pragma unroll
-            for (int j = 0; j < V; ++j) s.x += v[i][j] = to_f(p.e[j]);
-        }
-    }
-    const float inv = 1.f / (float)C, mu = row_sum<TPR>(s).x * inv;
-    s = make_float2(0.f, 0.f);
+    for (int i = 0; i < E; ++i)
+        if (lane + i * TPR < items && on) p[i] = xr[lane + i * TPR];
+    constexpr int NP = P::kPairs;
+    float2 v[E][NP], s = both(0.f);
 #pragma unroll
     for (int i = 0; i < E; ++i)
         if (lane + i * TPR < items && on) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[i][j] -= mu;
-                s.x = fmaf(v[i][j], v[i][j], s.x);
+            for (int j = 0; j < NP; ++j) s = add2(s, v[i][j] = p[i].get(j));
+        }
+    const float inv = 1.f / (float)C, mu = row_sum<TPR>(s.x + s.y) * inv;
+    s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if (lane + i * TPR < items && on) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                v[i][j] = add2(v[i][j], make_float2(-mu, V > 1 ? -mu : 0.f));
+                s = fma2(v[i][j], v[i][j], s);
             }
         }
-    const float rs = 1.f / sqrtf(row_sum<TPR>(s).x * inv + eps);
+    const float rs = 1.f / sqrtf(row_sum<TPR>(s.x + s.y) * inv + eps);
     if (!on) return;
     const int64_t g = G == 1 ? 0 : r % G;
     const W* wr = reinterpret_cast<const W*>(w + g * C);
@@ -97,10 +86,10 @@ norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias
         const int c = lane + i * TPR;
         if (c < items) {
             const W wv = wr[c], bv = br[c];
-            P p;
+            P o;
 #pragma unroll
-            for (int j = 0; j < V; ++j) p.e[j] = T(fmaf(v[i][j] * rs, wv.e[j], bv.e[j]));
-            yr[c] = p;
+            for (int j = 0; j < NP; ++j) o.set(j, fma2(mul2(v[i][j], both(rs)), wv.get(j), bv.get(j)));
+            yr[c] = o;
         }
     }
     if (lane == 0) {
@@ -109,91 +98,117 @@ norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias
     }
 }
 
-// Blocks blockIdx.x of group blockIdx.y walk the group's rows; partial sums of
-// the weight gradients to part[(group * blocks + block)][2][C].
+// The backward pass holds two rows of weight-gradient sums, a row and the next one's loads in registers: 12 warps of
+// up to 170 registers an SM (at 128 registers and 16 warps it spilled and took 98 us where it takes XX).
+constexpr int kBwdThreads = 384;
+
+// Blocks blockIdx.x of group blockIdx.y walk the group's rows, the next row's loads in flight while a row is worked on;
+// partial sums of the weight gradients to part[(group * blocks + block)][2][C].
 template <typename T, int V, int TPR, int E>
-__global__ void __launch_bounds__(block_threads<TPR>())
-norm_bwd(const T* dy, const T* x, const float* __restrict__ w,
-         const float* __restrict__ mean, const float* __restrict__ rstd, T* dx,
-         float* __restrict__ part, int64_t rows, int C, int G) {
+__global__ void __launch_bounds__((block_threads<TPR, kBwdThreads>()), 1)
+norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __restrict__ mean,
+         const float* __restrict__ rstd, T* dx, float* __restrict__ part, int64_t rows, int C, int G) {
     using P = Piece<T, V>;
     using W = Piece<float, V>;
-    constexpr int kRows = block_threads<TPR>() / TPR;
+    constexpr int kThreads = block_threads<TPR, kBwdThreads>(), kRows = kThreads / TPR;
     const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR, items = C / V, g = blockIdx.y;
-    const int64_t group_rows = rows / G;
+    const int64_t group_rows = rows / G, step = (int64_t)gridDim.x * kRows;
     const float inv = 1.f / (float)C;
-    float dw[E][V] = {}, db[E][V] = {};
+    constexpr int NP = P::kPairs;
+    float2 dw[E][NP], db[E][NP];
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) dw[i][j] = db[i][j] = both(0.f);
     const W* wr = reinterpret_cast<const W*>(w + (int64_t)g * C);
-    for (int64_t k = (int64_t)blockIdx.x * kRows; k < group_rows; k += (int64_t)gridDim.x * kRows) {
-        const bool on = k + sub < group_rows;
-        const int64_t r = on ? (k + sub) * G + g : 0;
+    struct Row {
+        P x[E], d[E];
+        float mu, rs;
+    };
+    auto fetch = [&](Row& q, int64_t k) {
+        if (k >= group_rows) return;
+        const int64_t r = k * G + g;
         const P* xr = reinterpret_cast<const P*>(x + r * C);
         const P* dr = reinterpret_cast<const P*>(dy + r * C);
-        P xp[E], dp[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = lane + i * TPR;
-            if (c < items && on) {
-                xp[i] = xr[c];
-                dp[i] = dr[c];
+        for (int i = 0; i < E; ++i)
+            if (lane + i * TPR < items) {
+                q.x[i] = xr[lane + i * TPR];
+                q.d[i] = dr[lane + i * TPR];
             }
-        }
-        const float mu = on ? mean[r] : 0.f, rs = on ? rstd[r] : 0.f;
-        float2 s = make_float2(0.f, 0.f);
-        float gv[E][V], xh[E][V];
+        q.mu = mean[r];
+        q.rs = rstd[r];
+    };
+    constexpr bool kAhead = E * V <= 24;  // where the registers allow it
+    Row row;
+    if (kAhead) fetch(row, (int64_t)blockIdx.x * kRows + sub);
+    for (int64_t k0 = (int64_t)blockIdx.x * kRows; k0 < group_rows; k0 += step) {
+        const int64_t k = k0 + sub;
+        const bool on = k < group_rows;
+        Row next;
+        if (kAhead)
+            fetch(next, k + step);
+        else
+            fetch(row, k);
+        float2 s1 = both(0.f), s2 = both(0.f);
+        const float2 rs = both(row.rs), shift = make_float2(-row.mu, V > 1 ? -row.mu : 0.f);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = lane + i * TPR;
-            if (c < items && on) {
-                const W wv = wr[c];
+        for (int i = 0; i < E; ++i)
+            if (lane + i * TPR < items && on) {
+                const W wv = wr[lane + i * TPR];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = to_f(dp[i].e[j]);
-                    xh[i][j] = (to_f(xp[i].e[j]) - mu) * rs;
-                    gv[i][j] = d * wv.e[j];
-                    dw[i][j] = fmaf(d, xh[i][j], dw[i][j]);
-                    db[i][j] += d;
-                    s.x += gv[i][j];
-                    s.y = fmaf(gv[i][j], xh[i][j], s.y);
+                for (int j = 0; j < NP; ++j) {
+                    const float2 d = row.d[i].get(j), xh = mul2(add2(row.x[i].get(j), shift), rs), gv = mul2(d, wv.get(j));
+                    dw[i][j] = fma2(d, xh, dw[i][j]);
+                    db[i][j] = add2(db[i][j], d);
+                    s1 = add2(s1, gv);
+                    s2 = fma2(gv, xh, s2);
                 }
             }
-        }
-        s = row_sum<TPR>(s);
-        const float m1 = s.x * inv, m2 = s.y * inv;
+        const float m1 = row_sum<TPR>(s1.x + s1.y) * inv, m2 = row_sum<TPR>(s2.x + s2.y) * inv;
         if (on) {
-            P* o = reinterpret_cast<P*>(dx + r * C);
+            P* o = reinterpret_cast<P*>(dx + (k * G + g) * C);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = lane + i * TPR;
-                if (c < items) {
-                    P p;
+            for (int i = 0; i < E; ++i)
+                if (lane + i * TPR < items) {
+                    const W wv = wr[lane + i * TPR];
+                    P q;
 #pragma unroll
-                    for (int j = 0; j < V; ++j) p.e[j] = T(rs * (gv[i][j] - m1 - xh[i][j] * m2));
-                    o[c] = p;
+                    for (int j = 0; j < NP; ++j) {
+                        const float2 xh = mul2(add2(row.x[i].get(j), shift), rs);
+                        const float2 c = fma2(row.d[i].get(j), wv.get(j), both(-m1));
+                        q.set(j, mul2(rs, fma2(xh, both(-m2), c)));
+                    }
+                    o[lane + i * TPR] = q;
                 }
-            }
         }
+        if (kAhead) row = next;
     }
     // over the block's rows, then out
     float* out = part + ((int64_t)g * gridDim.x + blockIdx.x) * 2 * C;
     if constexpr (kRows > 1) {
-        __shared__ float red[block_threads<TPR>()];
+        __shared__ float red[kRows][TPR * E * V];
 #pragma unroll
-        for (int i = 0; i < E; ++i)
+        for (int q = 0; q < 2; ++q) {
+            __syncthreads();
 #pragma unroll
-            for (int j = 0; j < V; ++j)
+            for (int i = 0; i < E; ++i)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    __syncthreads();
-                    red[threadIdx.x] = q ? db[i][j] : dw[i][j];
-                    __syncthreads();
-                    const int c = lane + i * TPR;
-                    if (sub == 0 && c < items) {
-                        float t = 0.f;
-                        for (int k = 0; k < kRows; ++k) t += red[k * TPR + lane];
-                        out[q * C + c * V + j] = t;
-                    }
+                for (int j = 0; j < V; ++j) {
+                    const float2 u = q ? db[i][j / 2] : dw[i][j / 2];
+                    red[sub][(i * V + j) * TPR + lane] = j & 1 ? u.y : u.x;
                 }
+            __syncthreads();
+            for (int e = threadIdx.x; e < TPR * E * V; e += kThreads) {
+                const int l = e % TPR, j = e / TPR % V, i = e / TPR / V, c = l + i * TPR;
+                if (c < items) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kRows; ++k) v += red[k][e];
+                    out[q * C + c * V + j] = v;
+                }
+            }
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -201,31 +216,33 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w,
             if (c < items)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    out[c * V + j] = dw[i][j];
-                    out[C + c * V + j] = db[i][j];
+                    out[c * V + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+                    out[C + c * V + j] = j & 1 ? db[i][j / 2].y : db[i][j / 2].x;
                 }
         }
     }
 }
 
-// dw, db [G][C] from the blocks' partial sums: 32 columns x 8 threads a block, in a fixed order
-__global__ void __launch_bounds__(256) norm_reduce(const float* __restrict__ part, float* __restrict__ dw,
-                                                   float* __restrict__ db, int blocks, int C) {
-    __shared__ float2 red[8][32];
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, k0 = threadIdx.x / 32, g = blockIdx.y;
+// dw, db [G][C] from the blocks' partial sums: 32 columns x 32 threads a block, in a fixed order
+__global__ void __launch_bounds__(1024) norm_reduce(const float* __restrict__ part, float* __restrict__ dw,
+                                                    float* __restrict__ db, int blocks, int C) {
+    __shared__ float2 red[32][32];
+    const int l = threadIdx.x % 32, c = blockIdx.x * 32 + l, k0 = threadIdx.x / 32, g = blockIdx.y;
     float2 s = make_float2(0.f, 0.f);
     if (c < C)
-        for (int k = k0; k < blocks; k += 8) {
+#pragma unroll 4
+        for (int k = k0; k < blocks; k += 32) {
             const float* p = part + ((int64_t)g * blocks + k) * 2 * C + c;
             s.x += p[0];
             s.y += p[C];
         }
-    red[k0][threadIdx.x % 32] = s;
+    red[k0][l] = s;
     __syncthreads();
     if (k0 == 0 && c < C) {
-        for (int k = 1; k < 8; ++k) {
-            s.x += red[k][threadIdx.x].x;
-            s.y += red[k][threadIdx.x].y;
+#pragma unroll 8
+        for (int k = 1; k < 32; ++k) {
+            s.x += red[k][l].x;
+            s.y += red[k][l].y;
         }
         dw[(int64_t)g * C + c] = s.x;
         db[(int64_t)g * C + c] = s.y;
@@ -252,14 +269,14 @@ struct BwdArgs {
 
 template <typename T, int V, int TPR, int E>
 cudaError_t fwd(const FwdArgs& a, cudaStream_t s) {
-    constexpr int kRows = block_threads<TPR>() / TPR;
-    norm_fwd<T, V, TPR, E><<<(unsigned)((a.rows + kRows - 1) / kRows), block_threads<TPR>(), 0, s>>>(
+    constexpr int kThreads = block_threads<TPR, 256>(), kRows = kThreads / TPR;
+    norm_fwd<T, V, TPR, E><<<(unsigned)((a.rows + kRows - 1) / kRows), kThreads, 0, s>>>(
         (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd, a.rows, a.C, a.G, a.eps);
     return cudaGetLastError();
 }
 template <typename T, int V, int TPR, int E>
 cudaError_t bwd(const BwdArgs& a, cudaStream_t s) {
-    norm_bwd<T, V, TPR, E><<<dim3(a.blocks, a.G), block_threads<TPR>(), 0, s>>>(
+    norm_bwd<T, V, TPR, E><<<dim3(a.blocks, a.G), block_threads<TPR, kBwdThreads>(), 0, s>>>(
         (const T*)a.dy, (const T*)a.x, a.w, a.mean, a.rstd, (T*)a.dx, a.part, a.rows, a.C, a.G);
     return cudaGetLastError();
 }
@@ -308,9 +325,9 @@ cudaError_t pick(int C, F f) {
     return C % V == 0 ? by_items<T, V>(C / V, f) : by_items<T, 1>(C, f);
 }
 
-// blocks a group of the backward pass: two an SM in all, no more than rows
+// blocks a group of the backward pass: one an SM in all, no more than rows
 inline int bwd_blocks(const fftconv_norm_s& p, int64_t rows) {
-    int64_t n = (2 * (int64_t)p.sms + p.groups - 1) / p.groups;
+    int64_t n = ((int64_t)p.sms + p.groups - 1) / p.groups;
     const int64_t most = rows / p.groups;
     n = n < most ? n : most;
     return (int)(n < 1 ? 1 : n);
@@ -336,7 +353,7 @@ cudaError_t launch_norm_bwd(const fftconv_norm_s& p, int64_t rows, const void* d
     cudaError_t e = p.dtype == FFTCONV_BF16 ? ln::pick<__nv_bfloat16>(p.C, ln::BwdPick{a, s})
                                             : ln::pick<float>(p.C, ln::BwdPick{a, s});
     if (e != cudaSuccess) return e;
-    ln::norm_reduce<<<dim3((p.C + 31) / 32, p.groups), 256, 0, s>>>(work, dw, db, a.blocks, p.C);
+    ln::norm_reduce<<<dim3((p.C + 31) / 32, p.groups), 1024, 0, s>>>(work, dw, db, a.blocks, p.C);
     return cudaGetLastError();
 }
 

@@ -352,6 +352,11 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
     if (p.s_out) store4(p.s_out + (size_t)bh * n + e, s);
 }
 
+cudaError_t launch_carry(const Args& a, int bh, int passes, const double* lg, cudaStream_t s) {
+    const unsigned blocks = (unsigned)((a.state_floats / 4 + kCarryThreads - 1) / kCarryThreads);
+    return launch<la_carry>(dim3(blocks, bh, passes), kCarryThreads, 0, s, true, a, lg);
+}
+
 template <int DX, int DZ>
 cudaError_t run(const Args& a, int bh, int passes, bool states, cudaStream_t s) {
     constexpr int bytes = Shape<DX, DZ>::kFloats * (int)sizeof(float);
@@ -520,20 +525,14 @@ cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t 
     }
     int dx, dz;
     padded(p, c.passes, &dx, &dz);
+    if (tc) return la::launch_tc(a, dx, dz, c.B, c.passes, ends, p, s);
     const int bh = c.B * p.H;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
     if (a.nseg > 1) {
-        e = tc ? la::launch_tc(a, dx, dz, c.B, c.passes, true, p, s) : la::launch_f32(a, dx, dz, bh, c.passes, true, s);
-        if (e != cudaSuccess) return e;
-        const unsigned blocks = (unsigned)((a.state_floats / 4 + la::kCarryThreads - 1) / la::kCarryThreads);
-        e = la::launch<la::la_carry>(dim3(blocks, bh, c.passes), la::kCarryThreads, 0, s, true, a, p.d_log);
-        if (e != cudaSuccess) return e;
+        e = la::launch_f32(a, dx, dz, bh, c.passes, true, s);
+        if (e == cudaSuccess) e = la::launch_carry(a, bh, c.passes, p.d_log, s);
     }
-    e = tc ? la::launch_tc(a, dx, dz, c.B, c.passes, false, p, s) : la::launch_f32(a, dx, dz, bh, c.passes, false, s);
-    // The tensor-core outputs' kernel keeps its state for the outputs alone: final states that a caller asks for come
-    // from the states' kernel, which sums them in fp32 (after the outputs: a caller may update its states in place).
-    if (e == cudaSuccess && tc && a.nseg == 1 && ends) e = la::launch_tc(a, dx, dz, c.B, c.passes, true, p, s);
-    return e;
+    return e == cudaSuccess ? la::launch_f32(a, dx, dz, bh, c.passes, false, s) : e;
 }
 
 cudaError_t launch_la_step(const fftconv_linattn_s& p, const LaStep& c, cudaStream_t s) {

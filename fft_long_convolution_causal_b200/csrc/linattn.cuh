@@ -60,8 +60,10 @@ cudaError_t launch(dim3 grid, int threads, size_t bytes, cudaStream_t s, bool ea
     return e;
 }
 
-// tcgen05 kernels (bf16): the segments' own states of the passes that carry them, or the outputs.
-cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool states, const fftconv_linattn_s& p,
+// Joins the segments' own states.
+cudaError_t launch_carry(const Args& a, int bh, int passes, const double* lg, cudaStream_t s);
+// The whole call on tcgen05 (bf16); ends: a pass returns its final states.
+cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool ends, const fftconv_linattn_s& p,
                       cudaStream_t s);
 
 }  // namespace la

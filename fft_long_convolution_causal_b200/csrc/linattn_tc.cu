@@ -371,6 +371,7 @@ la_main(const __grid_constant__ Args g) {
     um::fence_before();
     __syncthreads();
     um::fence_after();
+    la::let_next_start();
     const uint32_t tmem = m.tmem;
     const int quarter = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
@@ -784,6 +785,7 @@ la_states(const __grid_constant__ Args g) {
             }
             arrive(m.ufree[n & 1]);
         }
+        if (last) la::after_previous();  // the outputs' kernel has read the state that this may replace
         if (ok && mine) {
 #pragma unroll 1
             for (int n0 = 0; n0 < DZ; n0 += 16) {
@@ -870,25 +872,30 @@ void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int 
 }
 
 template <int DX, int DZ>
-cudaError_t run(const Args& g, int bh, int passes, bool states, cudaStream_t s) {
+cudaError_t run(const Args& g, int bh, int passes, bool ends, const double* lg, cudaStream_t s) {
+    using M = Main<DX, DZ>;
+    using S = States<DX, DZ>;
     const dim3 grid(g.a.nseg, bh, passes);
-    cudaError_t e;
-    if (states) {
-        using K = States<DX, DZ>;
-        if ((e = la::allow<la_states<DX, DZ>>((int)K::kBytes)) != cudaSuccess) return e;
-        return la::launch<la_states<DX, DZ>>(grid, K::kThreads, K::kBytes, s, false, g);
-    } else {
-        using K = Main<DX, DZ>;
-        if ((e = la::allow<la_main<DX, DZ>>((int)K::kBytes)) != cudaSuccess) return e;
-        return la::launch<la_main<DX, DZ>>(grid, K::kThreads, K::kBytes, s, g.a.nseg > 1, g);
+    const bool split = g.a.nseg > 1;
+    cudaError_t e = la::allow<la_main<DX, DZ>>((int)M::kBytes);
+    if (e == cudaSuccess && (split || ends)) e = la::allow<la_states<DX, DZ>>((int)S::kBytes);
+    if (e == cudaSuccess && split) {
+        e = la::launch<la_states<DX, DZ>>(grid, S::kThreads, S::kBytes, s, false, g);
+        if (e == cudaSuccess) e = la::launch_carry(g.a, bh, passes, lg, s);
     }
+    if (e == cudaSuccess) e = la::launch<la_main<DX, DZ>>(grid, M::kThreads, M::kBytes, s, split, g);
+    // The outputs' kernel keeps its state for the outputs alone: final states that a caller asks for come from the
+    // states' kernel, which sums them in fp32 (beside the outputs, but written after them: a caller may update its
+    // states in place).
+    if (e == cudaSuccess && !split && ends) e = la::launch<la_states<DX, DZ>>(grid, S::kThreads, S::kBytes, s, true, g);
+    return e;
 }
 
 }  // namespace latc
 
 namespace la {
 
-cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool states, const fftconv_linattn_s& p,
+cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool ends, const fftconv_linattn_s& p,
                       cudaStream_t s) {
     latc::Args g;
     g.a = a;
@@ -915,15 +922,15 @@ cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool sta
         g.x[i] = source(q.x, q.sx, q.dx);
         g.y[i] = source(q.y, q.sy, q.dx);
         g.z[i] = source(q.z, q.sz, q.dz);
-        if (!states) {
-            g.out[i] = source(q.out, q.so, q.dz);
-            if (g.src[g.out[i]].by_hand) return cudaErrorInvalidValue;
-        }
+        g.out[i] = source(q.out, q.so, q.dz);
+        if (g.src[g.out[i]].by_hand) return cudaErrorInvalidValue;
     }
     const int bh = B * a.H;
     if (dx <= 64)
-        return dz <= 64 ? latc::run<64, 64>(g, bh, passes, states, s) : latc::run<64, 128>(g, bh, passes, states, s);
-    return dz <= 64 ? latc::run<128, 64>(g, bh, passes, states, s) : latc::run<128, 128>(g, bh, passes, states, s);
+        return dz <= 64 ? latc::run<64, 64>(g, bh, passes, ends, p.d_log, s)
+                        : latc::run<64, 128>(g, bh, passes, ends, p.d_log, s);
+    return dz <= 64 ? latc::run<128, 64>(g, bh, passes, ends, p.d_log, s)
+                    : latc::run<128, 128>(g, bh, passes, ends, p.d_log, s);
 }
 
 }  // namespace la

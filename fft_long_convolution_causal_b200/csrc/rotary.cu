@@ -13,26 +13,13 @@
 #include <cuda_bf16.h>
 
 #include "mixer.h"
+#include "pairs.cuh"
 
 namespace fftc {
 namespace rot {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // heads whose loads are in flight together
-
-template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-    static constexpr int kN = 4;
-};
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int kN = 8;
-};
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+constexpr int kAhead = 2;  // heads whose loads are in flight together
 
 struct Args {
     RotaryView v[2];
@@ -43,15 +30,9 @@ struct Args {
     float m;
 };
 
-// V elements as one piece of memory (16 bytes, or one element)
-template <typename T, int V>
-struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16) Piece {
-    T e[V];
-};
-
 // V = elements of a 16-byte piece, or 1: an unaligned shape
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 4) rotary(const __grid_constant__ Args a) {
     using P = Piece<T, V>;
     constexpr int NP = INTER && V > 1 ? V / 2 : V;  // pairs of an item
     const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -74,20 +55,12 @@ __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Args 
         for (int h = h0; h < h1; ++h) *reinterpret_cast<P*>(to(h) + e) = *reinterpret_cast<const P*>(from(h) + e);
         return;
     }
-    float cs[NP], sn[NP];
-    const uint64_t pos = (uint64_t)a.pos[b * a.pos_stride + n];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const uint64_t ph = pos * a.turns[item * NP + i];  // turns modulo 1, exactly
-        sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-        cs[i] *= a.m;
-        sn[i] *= a.inverse ? -a.m : a.m;
-    }
     // offsets of the two pieces of an item; one piece when the pairs are neighbours
     constexpr bool kOne = INTER && V > 1;
     const int e0 = INTER ? 2 * NP * item : NP * item, e1 = INTER ? e0 + 1 : e0 + a.rot / 2;
-    for (int h = h0; h < h1; h += kAhead) {
-        P u[kAhead], w[kAhead];
+    // the first heads' loads are in flight while the sines are computed
+    P u[kAhead], w[kAhead];
+    auto fetch = [&](int h) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (h + k < h1) {
@@ -95,27 +68,53 @@ __global__ void __launch_bounds__(kThreads) rotary(const __grid_constant__ Args 
                 u[k] = *reinterpret_cast<const P*>(x + e0);
                 if (!kOne) w[k] = *reinterpret_cast<const P*>(x + e1);
             }
+    };
+    fetch(h0);
+    // pairs of neighbours: cosines twice each, the sine negated for the first; pairs apart: by two
+    constexpr int NQ = kOne ? P::kPairs : (NP + 1) / 2;
+    float2 cs[NQ], sn[NQ];
+    const uint64_t pos = (uint64_t)a.pos[b * a.pos_stride + n];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint64_t ph = pos * a.turns[item * NP + i];  // turns modulo 1, exactly
+        float s, c;
+        sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &s, &c);
+        c *= a.m;
+        s *= a.inverse ? -a.m : a.m;
+        if (kOne) {
+            cs[i] = both(c);
+            sn[i] = make_float2(-s, s);
+        } else if (i & 1) {
+            cs[i / 2].y = c;
+            sn[i / 2].y = s;
+        } else {
+            cs[i / 2] = make_float2(c, 0.f);
+            sn[i / 2] = make_float2(s, 0.f);
+        }
+    }
+    for (int h = h0;;) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (h + k < h1) {
                 T* y = to(h + k);
-                P r = u[k], t = w[k];
+                P r, t;
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const float x1 = to_f(kOne ? u[k].e[(2 * i) % V] : u[k].e[i % V]);
-                    const float x2 = to_f(kOne ? u[k].e[(2 * i + 1) % V] : w[k].e[i % V]);
-                    const T y1 = T(x1 * cs[i] - x2 * sn[i]), y2 = T(x2 * cs[i] + x1 * sn[i]);
+                for (int i = 0; i < NQ; ++i) {
+                    const float2 x1 = u[k].get(i);
                     if (kOne) {
-                        r.e[(2 * i) % V] = y1;
-                        r.e[(2 * i + 1) % V] = y2;
+                        r.set(i, fma2(x1, cs[i], mul2(make_float2(x1.y, x1.x), sn[i])));
                     } else {
-                        r.e[i % V] = y1;
-                        t.e[i % V] = y2;
+                        const float2 x2 = w[k].get(i);
+                        r.set(i, fma2(x1, cs[i], mul2(x2, make_float2(-sn[i].x, -sn[i].y))));
+                        t.set(i, fma2(x2, cs[i], mul2(x1, sn[i])));
                     }
                 }
                 *reinterpret_cast<P*>(y + e0) = r;
                 if (!kOne) *reinterpret_cast<P*>(y + e1) = t;
             }
+        h += kAhead;
+        if (h >= h1) break;
+        fetch(h);
     }
 }
 
@@ -124,18 +123,17 @@ cudaError_t run(Args a, int sms, bool copy_rest, cudaStream_t s) {
     constexpr int NP = INTER && V > 1 ? V / 2 : V;
     a.per_token = a.rot / 2 / NP + (copy_rest ? (a.dim - a.rot) / V : 0);
     const int64_t threads = a.tokens * a.per_token;
-    // heads a thread walks: as many as leave the SMs full (the sines are then computed once for all)
-    int groups = (int)((int64_t)sms * 2048 / threads);
-    groups = groups < 1 ? 1 : groups > a.H ? a.H : groups;
-    a.heads_per = (a.H + groups - 1) / groups;
-    groups = (a.H + a.heads_per - 1) / a.heads_per;
+    // Heads a thread walks: 8 share their sines; one each where few threads are there to fill the SMs.
+    const int64_t most = threads * a.H;
+    a.heads_per = most >= (int64_t)sms * 8192 ? 8 : most >= (int64_t)sms * 4096 ? 4 : 1;
+    const int groups = (a.H + a.heads_per - 1) / a.heads_per;
     rotary<T, V, INTER><<<dim3((unsigned)((threads + kThreads - 1) / kThreads), groups), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t pick(const fftconv_rotary_s& p, Args& a, int views, cudaStream_t s) {
-    constexpr int V = Vec<T>::kN;
+    constexpr int V = 16 / sizeof(T);
     bool vec = a.dim % V == 0 && (p.interleaved ? a.rot % V == 0 : (a.rot / 2) % V == 0), rest = a.dim > a.rot;
     bool same = true;
     for (int i = 0; i < views; ++i) {

@@ -11,8 +11,10 @@ streams and captured graphs never share scratch memory.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -22,28 +24,12 @@ from .binding import DTYPES, TORCH_DTYPES, _check, load_library
 _vp = ctypes.c_void_p
 
 
-class _Strides(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
-
-
-class _LinattnArgs(ctypes.Structure):
-    _fields_ = [("size", ctypes.c_size_t), ("B", ctypes.c_int), ("N", ctypes.c_int64), ("scale", ctypes.c_double),
-                ("q", _vp), ("k", _vp), ("v", _vp), ("sq", _Strides), ("sk", _Strides), ("sv", _Strides),
-                ("lengths", _vp), ("state_in", _vp), ("o", _vp), ("so", _Strides), ("state_out", _vp)]
-
-
-class _LinattnBwdArgs(ctypes.Structure):
-    _fields_ = [("size", ctypes.c_size_t), ("B", ctypes.c_int), ("N", ctypes.c_int64), ("scale", ctypes.c_double),
-                ("d_o", _vp), ("q", _vp), ("k", _vp), ("v", _vp),
-                ("sdo", _Strides), ("sq", _Strides), ("sk", _Strides), ("sv", _Strides),
-                ("lengths", _vp), ("state_in", _vp), ("d_state", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp),
-                ("sdq", _Strides), ("sdk", _Strides), ("sdv", _Strides), ("d_state_in", _vp)]
-
-
-class _LinattnStepArgs(ctypes.Structure):
-    _fields_ = [("size", ctypes.c_size_t), ("B", ctypes.c_int), ("slots_n", ctypes.c_int), ("scale", ctypes.c_double),
-                ("q", _vp), ("k", _vp), ("v", _vp), ("sq", _Strides), ("sk", _Strides), ("sv", _Strides),
-                ("slots", _vp), ("state", _vp), ("o", _vp), ("so", _Strides)]
+# Argument blocks of include/fftconv.h, packed in the C layout (a tenth of a ctypes structure's time); the library
+# checks their sizes.  3q: the strides of a tensor.
+_FWD = struct.Struct("@Niqd PPP 3q3q3q PP P3q P")
+_BWD = struct.Struct("@Niqd PPPP 3q3q3q3q PPP PPP 3q3q3q P")
+_STEP = struct.Struct("@Niid PPP 3q3q3q PP P3q")
+_ROTARY = struct.Struct("@Niqii Pqi PPPP 3q3q3q3q")
 
 
 class _RotaryOptions(ctypes.Structure):
@@ -52,19 +38,17 @@ class _RotaryOptions(ctypes.Structure):
                 ("factor", ctypes.c_double), ("context", ctypes.c_double)]
 
 
-class _RotaryArgs(ctypes.Structure):
-    _fields_ = [("size", ctypes.c_size_t), ("B", ctypes.c_int), ("N", ctypes.c_int64), ("H", ctypes.c_int),
-                ("H2", ctypes.c_int), ("positions", _vp), ("position_stride", ctypes.c_int64),
-                ("inverse", ctypes.c_int), ("x", _vp), ("x2", _vp), ("y", _vp), ("y2", _vp),
-                ("sx", _Strides), ("sx2", _Strides), ("sy", _Strides), ("sy2", _Strides)]
-
-
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}  # fftconv_rotary_scaling
 LAYOUTS = {"half": 0, "interleaved": 1}
 
 
-def _data(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+# the raw handle of the current stream of a device: a fraction of the time of building a Stream object
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _data(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 class _Mixer:
@@ -84,14 +68,15 @@ class _Mixer:
     def _make(self, create: str, *args):
         self.lib = load_library()
         h = ctypes.c_void_p()
-        self.device = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+        self._index = torch.cuda.current_device() if torch.cuda.is_available() else 0
+        self.device = torch.device("cuda", self._index)
         _check(getattr(self.lib, create)(ctypes.byref(h), *args), create)
         self._handle = h
 
     def _need(self, t, name: str, shape, dtype, contiguous: bool = True):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the plan on {self.device}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -100,28 +85,25 @@ class _Mixer:
         if contiguous and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
-    def _stream(self, stream):
-        return _vp((torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream)
+    def _view(self, t, name: str, shape):
+        """Strides of a [B, H, N, d] view of the plan's type (0 where a dimension has one element: its stride means
+        nothing)."""
+        self._need(t, name, shape, self.torch_dtype, False)
+        b, h, n, d = t.stride()
+        if d != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        B, H, N, _ = shape
+        return b if B > 1 else 0, h if H > 1 else 0, n if N > 1 else 0
+
+    def _stream(self, stream) -> int:
+        return _current_raw(self._index) if stream is None else stream.cuda_stream
 
     def _on(self, stream):
         """Allocations belong to the stream the work runs on."""
-        return torch.cuda.stream(stream)  # no-op for None
+        return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _strided(t: torch.Tensor, name: str) -> _Strides:
-    """Strides of a [B, H, N, d] view (0 where a dimension has one element: its stride means nothing)."""
-    (B, H, N, _), (b, h, n, d) = t.shape, t.stride()
-    if d != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Strides(b if B > 1 else 0, h if H > 1 else 0, n if N > 1 else 0)
-
-
-def _like(t: torch.Tensor, d: int) -> torch.Tensor:
-    """An empty [B, H, N, d] tensor, stored [B, N, H, d] where t is (its heads inside its tokens)."""
-    B, H, N, _ = t.shape
-    if t.stride(1) < t.stride(2):
-        return torch.empty(B, N, H, d, dtype=t.dtype, device=t.device).transpose(1, 2)
-    return torch.empty(B, H, N, d, dtype=t.dtype, device=t.device)
+_HERE = contextlib.nullcontext()
 
 
 class LinearAttentionPlan(_Mixer):
@@ -183,23 +165,18 @@ class LinearAttentionPlan(_Mixer):
         before the first token (None: zero); lengths [B] int32: tokens of each row,
         o is zero behind them."""
         B, N = self._tokens(q)
-        H, dt = self.H, self.torch_dtype
-        self._need(q, "q", (B, H, N, self.dk), dt, False)
-        self._need(k, "k", (B, H, N, self.dk), dt, False)
-        self._need(v, "v", (B, H, N, self.dv), dt, False)
+        H, dk, dv = self.H, self.dk, self.dv
+        sq, sk = self._view(q, "q", (B, H, N, dk)), self._view(k, "k", (B, H, N, dk))
+        sv = self._view(v, "v", (B, H, N, dv))
         self._optional(B, lengths, state=state)
         with self._on(stream):
             if o is None:
-                o = _like(v, self.dv)
-            else:
-                self._need(o, "o", (B, H, N, self.dv), dt, False)
-            out = torch.empty(B, H, self.dk, self.dv, dtype=torch.float32, device=self.device) if final_state else None
+                o = torch.empty_like(v)  # stored in the order of v's strides
+            out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=self.device) if final_state else None
             ws = self._workspace(0)
-        a = _LinattnArgs(ctypes.sizeof(_LinattnArgs), B, N, self.scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                         _strided(q, "q"), _strided(k, "k"), _strided(v, "v"), _data(lengths), _data(state),
-                         o.data_ptr(), _strided(o, "o"), _data(out))
-        _check(self.lib.fftconv_linattn_fwd(self._handle, ctypes.byref(a), _data(ws), self._stream(stream)),
-               "fftconv_linattn_fwd")
+        a = _FWD.pack(_FWD.size, B, N, self.scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), *sq, *sk, *sv,
+                      _data(lengths), _data(state), o.data_ptr(), *self._view(o, "o", (B, H, N, dv)), _data(out))
+        _check(self.lib.fftconv_linattn_fwd(self._handle, a, _data(ws), self._stream(stream)), "fftconv_linattn_fwd")
         return (o, out) if final_state else o
 
     def bwd(self, do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -209,23 +186,21 @@ class LinearAttentionPlan(_Mixer):
         dstate of the final states (None: zero): dq, dk, dv of the plan's dtype and,
         where state is given, dstate (fp32, of the initial states; else None)."""
         B, N = self._tokens(q)
-        H, dt = self.H, self.torch_dtype
-        for t, name, d in ((do, "do", self.dv), (q, "q", self.dk), (k, "k", self.dk), (v, "v", self.dv)):
-            self._need(t, name, (B, H, N, d), dt, False)
+        H, dk, dv = self.H, self.dk, self.dv
+        keys, values = (B, H, N, dk), (B, H, N, dv)
+        strides = (*self._view(do, "do", values), *self._view(q, "q", keys), *self._view(k, "k", keys),
+                   *self._view(v, "v", values))
         self._optional(B, lengths, state=state, dstate=dstate)
         with self._on(stream):
-            dq, dk, dv = _like(q, self.dk), _like(k, self.dk), _like(v, self.dv)
-            ds = torch.empty(B, H, self.dk, self.dv, dtype=torch.float32, device=self.device) \
-                if state is not None else None
+            gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+            ds = torch.empty((B, H, dk, dv), dtype=torch.float32, device=self.device) if state is not None else None
             ws = self._workspace(1)
-        a = _LinattnBwdArgs(ctypes.sizeof(_LinattnBwdArgs), B, N, self.scale, do.data_ptr(), q.data_ptr(),
-                            k.data_ptr(), v.data_ptr(), _strided(do, "do"), _strided(q, "q"), _strided(k, "k"),
-                            _strided(v, "v"), _data(lengths), _data(state), _data(dstate), dq.data_ptr(),
-                            dk.data_ptr(), dv.data_ptr(), _strided(dq, "dq"), _strided(dk, "dk"),
-                            _strided(dv, "dv"), _data(ds))
-        _check(self.lib.fftconv_linattn_bwd(self._handle, ctypes.byref(a), _data(ws), self._stream(stream)),
-               "fftconv_linattn_bwd")
-        return {"dq": dq, "dk": dk, "dv": dv, "dstate": ds}
+        a = _BWD.pack(_BWD.size, B, N, self.scale, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+                      _data(lengths), _data(state), _data(dstate), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+                      *self._view(gq, "dq", keys), *self._view(gk, "dk", keys), *self._view(gv, "dv", values),
+                      _data(ds))
+        _check(self.lib.fftconv_linattn_bwd(self._handle, a, _data(ws), self._stream(stream)), "fftconv_linattn_bwd")
+        return {"dq": gq, "dk": gk, "dv": gv, "dstate": ds}
 
     def step(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.Tensor,
              slots: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -248,21 +223,22 @@ class LinearAttentionPlan(_Mixer):
             raise ValueError(f"{B} rows, but {state.shape[0]} states")
         if o is None:
             with self._on(stream):
-                o = torch.empty(B, H, self.dv, dtype=dt, device=self.device)
+                o = torch.empty((B, H, self.dv), dtype=dt, device=self.device)
         else:
             self._need(o, "o", (B, H, self.dv), dt, False)
-        strides = []
-        for t, name in ((q, "q"), (k, "k"), (v, "v"), (o, "o")):
-            b, h, d = t.stride()
-            if d != 1:
-                raise ValueError(f"{name}: the last dimension must be contiguous")
-            strides.append(_Strides(b, h, 0))
-        a = _LinattnStepArgs(ctypes.sizeof(_LinattnStepArgs), B, state.shape[0], self.scale, q.data_ptr(),
-                             k.data_ptr(), v.data_ptr(), *strides[:3], _data(slots), state.data_ptr(), o.data_ptr(),
-                             strides[3])
-        _check(self.lib.fftconv_linattn_step(self._handle, ctypes.byref(a), self._stream(stream)),
-               "fftconv_linattn_step")
+        a = _STEP.pack(_STEP.size, B, state.shape[0], self.scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                       *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), _data(slots), state.data_ptr(), o.data_ptr(),
+                       *_rows(o, "o"))
+        _check(self.lib.fftconv_linattn_step(self._handle, a, self._stream(stream)), "fftconv_linattn_step")
         return o
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Strides of a [B, H, d] view."""
+    b, h, d = t.stride()
+    if d != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return b, h, 0
 
 
 class RotaryPlan(_Mixer):
@@ -290,26 +266,27 @@ class RotaryPlan(_Mixer):
         if not isinstance(x, torch.Tensor) or x.dim() != 4:
             raise ValueError("x must be [B, H, N, dim]")
         B, H, N, _ = x.shape
-        self._need(x, "x", (B, H, N, self.dim), self.torch_dtype, False)
+        dim = self.dim
+        sx, sx2, H2 = self._view(x, "x", (B, H, N, dim)), (0, 0, 0), 0
         if x2 is not None:
             if not isinstance(x2, torch.Tensor) or x2.dim() != 4:
                 raise ValueError("x2 must be [B, H, N, dim]")
-            self._need(x2, "x2", (B, x2.shape[1], N, self.dim), self.torch_dtype, False)
-        if positions is None:
+            H2 = x2.shape[1]
+            sx2 = self._view(x2, "x2", (B, H2, N, dim))
+        if not isinstance(positions, torch.Tensor):
             raise ValueError("positions are needed")
-        self._need(positions, "positions", (N,) if positions.dim() == 1 else (B, N), torch.int64)
+        flat = positions.dim() == 1
+        self._need(positions, "positions", (N,) if flat else (B, N), torch.int64)
         if inplace:
-            y, y2 = x, x2
+            y, y2, sy, sy2 = x, x2, sx, sx2
         else:
             with self._on(stream):
-                y, y2 = _like(x, self.dim), None if x2 is None else _like(x2, self.dim)
-        zero = _Strides(0, 0, 0)
-        a = _RotaryArgs(ctypes.sizeof(_RotaryArgs), B, N, H, 0 if x2 is None else x2.shape[1], positions.data_ptr(),
-                        0 if positions.dim() == 1 else N, int(inverse), x.data_ptr(), _data(x2), y.data_ptr(),
-                        _data(y2), _strided(x, "x"), zero if x2 is None else _strided(x2, "x2"), _strided(y, "y"),
-                        zero if x2 is None else _strided(y2, "y2"))
-        _check(self.lib.fftconv_rotary_apply(self._handle, ctypes.byref(a), self._stream(stream)),
-               "fftconv_rotary_apply")
+                y, y2 = torch.empty_like(x), None if x2 is None else torch.empty_like(x2)
+            sy = self._view(y, "y", (B, H, N, dim))
+            sy2 = sx2 if x2 is None else self._view(y2, "y2", (B, H2, N, dim))
+        a = _ROTARY.pack(_ROTARY.size, B, N, H, H2, positions.data_ptr(), 0 if flat else N, int(inverse),
+                         x.data_ptr(), _data(x2), y.data_ptr(), _data(y2), *sx, *sx2, *sy, *sy2)
+        _check(self.lib.fftconv_rotary_apply(self._handle, a, self._stream(stream)), "fftconv_rotary_apply")
         return y if x2 is None else (y, y2)
 
 
@@ -322,6 +299,7 @@ class LayerNormPlan(_Mixer):
         self.rows, self.C, self.dtype, self.groups, self.eps = rows, C, dtype, groups, eps
         self.torch_dtype = TORCH_DTYPES[dtype]
         self._make("fftconv_norm_plan_create", rows, C, groups, DTYPES[dtype], ctypes.byref(ctypes.c_double(eps)))
+        self._bytes = int(self.lib.fftconv_norm_bwd_workspace_bytes(self._handle))
 
     def _rows(self, x, name: str) -> int:
         if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] != self.C:
@@ -351,7 +329,7 @@ class LayerNormPlan(_Mixer):
             if y is None:
                 y = torch.empty_like(x)
             if statistics:
-                mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=self.device).unbind(0)
+                mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=self.device).unbind(0)
         _check(self.lib.fftconv_norm_fwd(self._handle, rows, x.data_ptr(), weight.data_ptr(), bias.data_ptr(),
                                          y.data_ptr(), _data(mean), _data(rstd), self._stream(stream)),
                "fftconv_norm_fwd")
@@ -367,9 +345,8 @@ class LayerNormPlan(_Mixer):
         self._need(rstd, "rstd", (rows,), torch.float32)
         with self._on(stream):
             dx = torch.empty_like(x)
-            dw, db = torch.empty(2, self.groups, self.C, dtype=torch.float32, device=self.device).unbind(0)
-            ws = torch.empty(int(self.lib.fftconv_norm_bwd_workspace_bytes(self._handle)), dtype=torch.uint8,
-                             device=self.device)
+            dw, db = torch.empty((2, self.groups, self.C), dtype=torch.float32, device=self.device).unbind(0)
+            ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         _check(self.lib.fftconv_norm_bwd(self._handle, rows, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
                                          mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(),
                                          db.data_ptr(), ws.data_ptr(), self._stream(stream)), "fftconv_norm_bwd")
@@ -402,7 +379,7 @@ class RetentionPlan:
         """y [B, N, H, dv] = norm(attention(rotary(q), rotary(k), v)); weight, bias
         [H, dv].  Returns y, then the final states if asked for, then with `save` what
         bwd needs.  (The norm of a row behind a length is its bias.)"""
-        with torch.cuda.stream(stream):
+        with self.attention._on(stream):
             qr, kr = self.rotary.apply(q, k, positions=positions, stream=stream)
             got = self.attention.fwd(qr, kr, v, state=state, lengths=lengths, final_state=final_state, stream=stream)
             o, end = got if final_state else (got, None)
@@ -417,7 +394,7 @@ class RetentionPlan:
         """Gradients for dy [B, N, H, dv]: dq, dk, dv, dweight, dbias and, where fwd had
         states, dstate."""
         qr, kr, v, state, lengths, positions, rows, mean, rstd = saved
-        with torch.cuda.stream(stream):
+        with self.attention._on(stream):
             do, dw, db = self.norm.bwd(dy, rows, weight, mean, rstd, stream=stream)
             g = self.attention.bwd(do.transpose(1, 2), qr, kr, v, state=state, dstate=dstate, lengths=lengths,
                                    stream=stream)
@@ -428,7 +405,7 @@ class RetentionPlan:
              positions: torch.Tensor, state: torch.Tensor, slots: Optional[torch.Tensor] = None,
              stream=None) -> torch.Tensor:
         """One token a row: y [B, H, dv] from q, k [B, H, dk], v [B, H, dv] at positions [B] int64."""
-        with torch.cuda.stream(stream):
+        with self.attention._on(stream):
             qr, kr = self.rotary.apply(q.unsqueeze(2), k.unsqueeze(2), positions=positions.unsqueeze(1),
                                        stream=stream)
             o = self.attention.step(qr.squeeze(2), kr.squeeze(2), v, state, slots=slots, stream=stream)
