@@ -49,52 +49,62 @@ norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias
     using W = Piece<float, V>;
     constexpr int kRows = block_threads<TPR, 256>() / TPR;
     const int lane = threadIdx.x % TPR, items = C / V;
-    const int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-    const bool on = r < rows;
-    const P* xr = reinterpret_cast<const P*>(x + (on ? r : 0) * C);
-    P p[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        if (lane + i * TPR < items && on) p[i] = xr[lane + i * TPR];
+    const int64_t step = (int64_t)gridDim.x * kRows;
     constexpr int NP = P::kPairs;
-    float2 v[E][NP], s = both(0.f);
+    const float inv = 1.f / (float)C;
+    P p[E];
+    auto fetch = [&](int64_t r) {
+        if (r >= rows) return;
+        const P* xr = reinterpret_cast<const P*>(x + r * C);
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-        if (lane + i * TPR < items && on) {
+        for (int i = 0; i < E; ++i)
+            if (lane + i * TPR < items) p[i] = xr[lane + i * TPR];
+    };
+    int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    fetch(r);
+    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += step, r += step) {
+        const bool on = r < rows;
+        float2 v[E][NP], s = both(0.f);
 #pragma unroll
-            for (int j = 0; j < NP; ++j) s = add2(s, v[i][j] = p[i].get(j));
-        }
-    const float inv = 1.f / (float)C, mu = row_sum<TPR>(s.x + s.y) * inv;
-    s = both(0.f);
+        for (int i = 0; i < E; ++i)
+            if (lane + i * TPR < items && on) {
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-        if (lane + i * TPR < items && on) {
+                for (int j = 0; j < NP; ++j) s = add2(s, v[i][j] = p[i].get(j));
+            }
+        fetch(r + step);  // in flight while this row is worked on
+        const float mu = row_sum<TPR>(s.x + s.y) * inv;
+        s = both(0.f);
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                v[i][j] = add2(v[i][j], make_float2(-mu, V > 1 ? -mu : 0.f));
-                s = fma2(v[i][j], v[i][j], s);
+        for (int i = 0; i < E; ++i)
+            if (lane + i * TPR < items && on) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    v[i][j] = add2(v[i][j], make_float2(-mu, V > 1 ? -mu : 0.f));
+                    s = fma2(v[i][j], v[i][j], s);
+                }
+            }
+        const float rs = 1.f / sqrtf(row_sum<TPR>(s.x + s.y) * inv + eps);
+        if (on) {
+            const int64_t g = G == 1 ? 0 : r % G;
+            const W* wr = reinterpret_cast<const W*>(w + g * C);
+            const W* br = reinterpret_cast<const W*>(bias + g * C);
+            P* yr = reinterpret_cast<P*>(y + r * C);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int c = lane + i * TPR;
+                if (c < items) {
+                    const W wv = wr[c], bv = br[c];
+                    P o;
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) o.set(j, fma2(mul2(v[i][j], both(rs)), wv.get(j), bv.get(j)));
+                    yr[c] = o;
+                }
+            }
+            if (lane == 0) {
+                if (mean) mean[r] = mu;
+                if (rstd) rstd[r] = rs;
             }
         }
-    const float rs = 1.f / sqrtf(row_sum<TPR>(s.x + s.y) * inv + eps);
-    if (!on) return;
-    const int64_t g = G == 1 ? 0 : r % G;
-    const W* wr = reinterpret_cast<const W*>(w + g * C);
-    const W* br = reinterpret_cast<const W*>(bias + g * C);
-    P* yr = reinterpret_cast<P*>(y + r * C);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int c = lane + i * TPR;
-        if (c < items) {
-            const W wv = wr[c], bv = br[c];
-            P o;
-#pragma unroll
-            for (int j = 0; j < NP; ++j) o.set(j, fma2(mul2(v[i][j], both(rs)), wv.get(j), bv.get(j)));
-            yr[c] = o;
-        }
-    }
-    if (lane == 0) {
-        if (mean) mean[r] = mu;
-        if (rstd) rstd[r] = rs;
     }
 }
 
@@ -257,6 +267,7 @@ struct FwdArgs {
     int64_t rows;
     int C, G;
     float eps;
+    int sms;
 };
 struct BwdArgs {
     const void *dy, *x;
@@ -270,7 +281,17 @@ struct BwdArgs {
 template <typename T, int V, int TPR, int E>
 cudaError_t fwd(const FwdArgs& a, cudaStream_t s) {
     constexpr int kThreads = block_threads<TPR, 256>(), kRows = kThreads / TPR;
-    norm_fwd<T, V, TPR, E><<<(unsigned)((a.rows + kRows - 1) / kRows), kThreads, 0, s>>>(
+    // the blocks that the SMs hold at once, each walking rows
+    static const int held = [] {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_fwd<T, V, TPR, E>, kThreads, 0) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        return n > 0 ? n : 1;
+    }();
+    const int64_t blocks = (a.rows + kRows - 1) / kRows, most = (int64_t)a.sms * held;
+    norm_fwd<T, V, TPR, E><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, s>>>(
         (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd, a.rows, a.C, a.G, a.eps);
     return cudaGetLastError();
 }
@@ -337,7 +358,7 @@ inline int bwd_blocks(const fftconv_norm_s& p, int64_t rows) {
 
 cudaError_t launch_norm_fwd(const fftconv_norm_s& p, int64_t rows, const void* x, const float* w, const float* b,
                             void* y, float* mean, float* rstd, cudaStream_t s) {
-    const ln::FwdArgs a{x, w, b, y, mean, rstd, rows, p.C, p.groups, p.eps};
+    const ln::FwdArgs a{x, w, b, y, mean, rstd, rows, p.C, p.groups, p.eps, p.sms};
     return p.dtype == FFTCONV_BF16 ? ln::pick<__nv_bfloat16>(p.C, ln::FwdPick{a, s})
                                    : ln::pick<float>(p.C, ln::FwdPick{a, s});
 }
