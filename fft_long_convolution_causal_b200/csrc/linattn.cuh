@@ -11,13 +11,18 @@ namespace la {
 
 struct Args {
     LaPass p[kLaMaxPasses];
-    int H, nseg;
+    int H, nseg, passes;
     int64_t N, seg;             // tokens, tokens a segment
     const int32_t* lengths;
     const float* pw;            // [H][kLaPowers]
     float* work;                // [pass][bh][nseg][dk * dv]: segment states
     size_t pass_floats, state_floats;
 };
+
+// Block x runs pass x mod passes of segment x / passes: the passes of one (row, head) run side by side and find each
+// other's tensors in L2.
+__device__ __forceinline__ int pass_of(const Args& a) { return a.passes == 1 ? 0 : (int)blockIdx.x % a.passes; }
+__device__ __forceinline__ int segment_of(const Args& a) { return a.passes == 1 ? (int)blockIdx.x : (int)blockIdx.x / a.passes; }
 
 __device__ __forceinline__ int64_t live_tokens(const Args& a, int b) {
     if (!a.lengths) return a.N;

@@ -176,7 +176,7 @@ struct Copier {
     // gave up.
     __device__ __forceinline__ bool operator()(int what, int blocks, int n, uint32_t dst, const uint64_t& full,
                                                const uint64_t& empty, int use) const {
-        const int lane = threadIdx.x & 31, pass = blockIdx.z;
+        const int lane = threadIdx.x & 31, pass = la::pass_of(g.a);
         if (use > 0 && !wait.all(empty, (uint32_t)(use - 1) & 1u)) return false;
         const int64_t t0 = sp.start(n);
         const int L = sp.tokens(n);
@@ -281,9 +281,8 @@ struct Main {
     static constexpr bool kTwo = DX == 64 && DZ == 64;  // two CTAs an SM
     static constexpr uint32_t kTX = (uint32_t)DX * 256u, kTZ = (uint32_t)DZ * 256u;  // bytes of a tile
     static constexpr uint32_t kS = (uint32_t)DX * DZ * 2u, kLo = kTX;
-    // Tiles: two of y, one of x, two of z.  x is done with after inter, y after the state's product, z after the
+    // Five tiles: two of y, one of x, two of z.  x is done with after inter, y after the state's product, z after the
     // output staged in it has left: the next x, the next z and the y after next are requested in that order.
-    static constexpr int kTiles = 5;
     // The state's product has 128 rows whatever DX is: with DX = 64 its descriptor reads 16 KiB behind
     // a term of y (rows nobody looks at), which has to be this CTA's memory.
     static constexpr uint32_t kOffLo = 3 * kTX + 2 * kTZ, kOffS = kOffLo + kLo, kOffTail = kOffS + kS;
@@ -291,11 +290,14 @@ struct Main {
     static constexpr uint32_t kBytes = kOffTail + kTail;
     // tensor-memory columns: scores, O, the state.  P' (bf16) replaces the first quarter of each half of the scores:
     // the two warps of a row each overwrite only what they have read.
-    static constexpr uint32_t kP = 0, kO = 128, kST = kO + DZ, kCols = DZ == 64 ? 256 : 512;
+    // Where it has room, inter and intra have accumulators of their own and meet in the output's registers; where it
+    // has not (two CTAs an SM), intra adds to inter's, whose rows are scaled in place first.
+    static constexpr bool kApart = !kTwo;
+    static constexpr uint32_t kP = 0, kO = 128, kOI = kApart ? kO + DZ : kO, kST = kOI + DZ, kCols = kTwo ? 256 : 512;
     static constexpr int kThreads = 3 * 128 + 64;
 };
 struct MainTail {
-    uint64_t xy[2], zfull[2], empty[5], pfull, pored, iready, ifull, ofull, staged, yfull, sdone, drain;
+    uint64_t xy[2], zfull[2], empty[3], pfull, pored, iready, ifull, ofull, staged[2], yfull, sdone, drain;
     alignas(16) float ct[32];  // read four at a time
     float pw[kLaPowers], dt[64];
     uint32_t tmem;
@@ -310,44 +312,66 @@ la_main(const __grid_constant__ Args g) {
     extern __shared__ __align__(1024) uint8_t smem[];
     MainTail& m = *reinterpret_cast<MainTail*>(smem + K::kOffTail);
     const la::Args& a = g.a;
-    const LaPass& p = a.p[blockIdx.z];
+    const int pass = la::pass_of(a);
+    const LaPass& p = a.p[pass];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+    const int sg = la::segment_of(a), bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
     const Span sp(a, p, sg, b);
     const bool rev = sp.rev;
     const int nch = sp.nch;
     const uint32_t sb = smem_u32(smem);
     const Waiter wait{&m.abort, g.limit};
     constexpr int kMmaWarp = 12, kCopyWarp = 13;
-    // tile `item` (0 y, 1 x, 2 z) of chunk n: its place, how often that was used before, and where it is
-    auto slot = [](int n, int item) { return item == 1 ? 2 : item == 0 ? n & 1 : 3 + (n & 1); };
+    // tile `item` (0 y, 1 x, 2 z) of chunk n: its barrier, how often its place was used before, and where that is
+    auto slot = [](int n, int item) { return item == 1 ? 2 : n & 1; };
     auto use = [](int n, int item) { return item == 1 ? n : n >> 1; };
     auto tile = [&](int n, int item) {
         return sb + (item == 1 ? 2 * K::kTX : item == 0 ? (uint32_t)(n & 1) * K::kTX : 3 * K::kTX + (uint32_t)(n & 1) * K::kTZ);
     };
     const Copier copy{g, p, sp, b, h, wait};
     auto load = [&](int n, int item) {
-        return n >= nch || copy(item, (item == 2 ? DZ : DX) / 64, n, tile(n, item), item == 2 ? m.zfull[n & 1] : m.xy[n & 1],
-                                m.empty[slot(n, item)], use(n, item));
+        if (n >= nch) return true;
+        // z's place is free once the outputs staged there have left (this warp's own bulk copy)
+        if (item == 2) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+        }
+        return copy(item, (item == 2 ? DZ : DX) / 64, n, tile(n, item), item == 2 ? m.zfull[n & 1] : m.xy[n & 1],
+                    m.empty[item == 2 ? 0 : slot(n, item)], item == 2 ? 0 : use(n, item));
     };
-    // the order of the copies: y0, then x, z of chunk n and y of chunk n + 1
+    // the outputs of chunk n, staged in z's tile, go out as a bulk copy
+    auto store = [&](int n) {
+        if (!wait.all(m.staged[n & 1], (uint32_t)(n >> 1) & 1u)) return false;
+        if (lane == 0) {
+            const Source& so = g.src[g.out[pass]];
+            const int tk = (int)(sp.first + sp.start(n));
+            const int c1 = so.at(1, tk, h, b), c2 = so.at(2, tk, h, b), c3 = so.at(3, tk, h, b);
+#pragma unroll 1
+            for (int k = 0; k < DZ / 64; ++k)
+                if (64 * k < p.dz) tma_store_4d(&so.map, tile(n, 2) + (uint32_t)k * kBlock, 64 * k, c1, c2, c3);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        __syncwarp();
+        return true;
+    };
+    // the order of the copies: y0, then x, z of chunk k, y of chunk k + 1 and the outputs of chunk k - 1
     auto load_next = [&](int i) {
         const int k = i ? (i - 1) / 3 : -1, r = i ? (i - 1) % 3 : 2;
-        return r == 2 ? load(k + 1, 0) : load(k, r + 1);
+        return r == 2 ? load(k + 1, 0) && (k < 1 || store(k - 1)) : load(k, r + 1);
     };
 
     if (tid == 32 * kCopyWarp) {
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(smem_u32(&m.xy[i]), 2);
             um::mbar_init(smem_u32(&m.zfull[i]), 1);
+            um::mbar_init(smem_u32(&m.staged[i]), 4);  // two: a chunk may be staged before the last one is seen
         }
-        for (int i = 0; i < K::kTiles; ++i) um::mbar_init(smem_u32(&m.empty[i]), 1);
+        for (int i = 0; i < 3; ++i) um::mbar_init(smem_u32(&m.empty[i]), 1);
         um::mbar_init(smem_u32(&m.pfull), 1);
-        um::mbar_init(smem_u32(&m.pored), 12);  // P' in place, O's rows scaled
+        um::mbar_init(smem_u32(&m.pored), K::kApart ? 8 : 12);  // P' in place, O's rows scaled
         um::mbar_init(smem_u32(&m.iready), 4);  // the state decayed and copied, O read
         um::mbar_init(smem_u32(&m.ifull), 1);
         um::mbar_init(smem_u32(&m.ofull), 1);
-        um::mbar_init(smem_u32(&m.staged), 4);
         um::mbar_init(smem_u32(&m.yfull), 8);
         um::mbar_init(smem_u32(&m.sdone), 1);
         um::mbar_init(smem_u32(&m.drain), 1);
@@ -390,8 +414,8 @@ la_main(const __grid_constant__ Args g) {
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < DX / 16; ++k)
-                        um::mma_ss(tmem + K::kO, kx + kstep(k), ds + (uint64_t)(k * 16), id_inter, k > 0);
-                    um::mma_commit(smem_u32(&m.ifull));
+                        um::mma_ss(tmem + K::kOI, kx + kstep(k), ds + (uint64_t)(k * 16), id_inter, k > 0);
+                    if (!K::kApart) um::mma_commit(smem_u32(&m.ifull));
                     um::mma_commit(smem_u32(&m.empty[2]));
                 }
                 __syncwarp();
@@ -400,7 +424,7 @@ la_main(const __grid_constant__ Args g) {
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < kC / 16; ++k)
-                        um::mma_ts(tmem + K::kO, tmem + K::kP + (k / 4) * 64u + (k % 4) * 8u, zz + mnstep(k), id_inter, 1);
+                        um::mma_ts(tmem + K::kO, tmem + K::kP + (k / 4) * 64u + (k % 4) * 8u, zz + mnstep(k), id_inter, !K::kApart || k > 0);
                     um::mma_commit(smem_u32(&m.ofull));
                 }
                 __syncwarp();
@@ -440,6 +464,8 @@ la_main(const __grid_constant__ Args g) {
         int i = kFirst;
 #pragma unroll 1
         for (; i <= 3 * nch && ok; ++i) ok = load_next(i);
+        if (ok && nch) ok = store(nch - 1);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok || *wait.abort) {  // the last two chunks' copies may be in flight
             const int n = (i + 2) / 3;
             for (int c = n > 1 ? n - 1 : 0; c <= n && c < nch; ++c) {
@@ -452,8 +478,7 @@ la_main(const __grid_constant__ Args g) {
         const int d = 32 * quarter + lane;
         const bool mine = 32 * quarter < DX;  // this warp's lanes hold rows of the state
         const uint32_t ts = tl + K::kST;
-        const Source& so = g.src[g.out[blockIdx.z]];
-        const float* s0 = p.carried ? a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats
+        const float* s0 = p.carried ? a.work + pass * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats
                           : p.s_in    ? p.s_in + (size_t)bh * p.dx * p.dz
                                       : nullptr;
         la::after_previous();  // the states entering the segments
@@ -469,19 +494,7 @@ la_main(const __grid_constant__ Args g) {
 #pragma unroll
             for (int c = 0; c < DZ / 8; ++c) sts128(tz + tile_off(d, c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             um::fence_proxy_async();
-            arrive(m.staged);
-            if (warp == 4) {
-                if (!wait.all(m.staged, (uint32_t)n & 1u)) return;
-                if (lane == 0) {
-                    const int tk = (int)(sp.first + sp.start(n));
-                    const int c1 = so.at(1, tk, h, b), c2 = so.at(2, tk, h, b), c3 = so.at(3, tk, h, b);
-#pragma unroll 1
-                    for (int k = 0; k < DZ / 64; ++k)
-                        if (64 * k < p.dz) tma_store_4d(&so.map, tz + (uint32_t)k * kBlock, 64 * k, c1, c2, c3);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                }
-                __syncwarp();
-            }
+            arrive(m.staged[n & 1]);
         };
         bool ok = true;
 #pragma unroll 1
@@ -510,22 +523,20 @@ la_main(const __grid_constant__ Args g) {
             arrive(m.iready);
             if (n) stage(n - 1);
             const float fo = p.s_i * (rev ? m.pw[max(L - 1 - d, 0)] : m.pw[d + 1]);
-            if (!(ok = wait.all(m.ifull, (uint32_t)n & 1u))) break;
-            um::fence_after();
+            if (!K::kApart) {
+                if (!(ok = wait.all(m.ifull, (uint32_t)n & 1u))) break;
+                um::fence_after();
 #pragma unroll 1
-            for (int n0 = 0; n0 < DZ; n0 += 16) {
-                uint32_t r[16];
-                um::ld32x32_x16(tl + K::kO + n0, r);
-                um::wait_ld<16>(r);
+                for (int n0 = 0; n0 < DZ; n0 += 16) {
+                    uint32_t r[16];
+                    um::ld32x32_x16(tl + K::kO + n0, r);
+                    um::wait_ld<16>(r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = as_u(fo * as_f(r[i]));
-                um::st32x32_x16(tl + K::kO + n0, r);
-            }
-            um::wait_st();
-            arrive(m.pored);
-            if (n && warp == 4 && lane == 0) {  // the last chunk's outputs have left z's tile
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                um::mbar_arrive(smem_u32(&m.empty[3 + ((n - 1) & 1)]));
+                    for (int i = 0; i < 16; ++i) r[i] = as_u(fo * as_f(r[i]));
+                    um::st32x32_x16(tl + K::kO + n0, r);
+                }
+                um::wait_st();
+                arrive(m.pored);
             }
             if (!(ok = wait.all(m.ofull, (uint32_t)n & 1u))) break;
             um::fence_after();
@@ -533,7 +544,16 @@ la_main(const __grid_constant__ Args g) {
             for (int n0 = 0; n0 < DZ; n0 += 16) {
                 uint32_t r[16];
                 um::ld32x32_x16(tl + K::kO + n0, r);
-                um::wait_ld<16>(r);
+                if (K::kApart) {
+                    uint32_t ri[16];
+                    um::ld32x32_x16(tl + K::kOI + n0, ri);
+                    um::wait_ld<16>(r);
+                    um::wait_ld<16>(ri);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = as_u(fmaf(fo, as_f(ri[i]), as_f(r[i])));
+                } else {
+                    um::wait_ld<16>(r);
+                }
                 // rows behind the length are zeros
 #pragma unroll
                 for (int c = 0; c < 8; ++c) o[n0 / 2 + c] = d < L ? pack2(as_f(r[2 * c]), as_f(r[2 * c + 1])) : 0u;
@@ -542,7 +562,6 @@ la_main(const __grid_constant__ Args g) {
             um::fence_after();
         }
         if (ok && nch) stage(nch - 1);
-        if (warp == 4 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
         // ================================================ scores -> P', and the split of y
         const int i = 32 * quarter + lane, part = warp >> 3;  // row (then token), half of its columns
@@ -641,10 +660,11 @@ la_states(const __grid_constant__ Args g) {
     extern __shared__ __align__(1024) uint8_t smem[];
     StatesTail& m = *reinterpret_cast<StatesTail*>(smem + K::kOffTail);
     const la::Args& a = g.a;
-    const LaPass& p = a.p[blockIdx.z];
+    const int pass = la::pass_of(a);
+    const LaPass& p = a.p[pass];
     if (!p.carried && !p.s_out) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sg = blockIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+    const int sg = la::segment_of(a), bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
     const Span sp(a, p, sg, b);
     const int nch = sp.nch;
     const uint32_t sb = smem_u32(smem);
@@ -754,7 +774,7 @@ la_states(const __grid_constant__ Args g) {
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16), ts = tl + K::kST;
         const bool last = a.nseg == 1;  // the whole row: its final state, from the initial one
         float* out = (last ? p.s_out + (size_t)bh * p.dx * p.dz
-                           : a.work + blockIdx.z * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats) +
+                           : a.work + pass * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats) +
                      (size_t)d * p.dz;
         const float* s0 = last && p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
         if (mine) {
@@ -875,7 +895,7 @@ template <int DX, int DZ>
 cudaError_t run(const Args& g, int bh, int passes, bool ends, const double* lg, cudaStream_t s) {
     using M = Main<DX, DZ>;
     using S = States<DX, DZ>;
-    const dim3 grid(g.a.nseg, bh, passes);
+    const dim3 grid(g.a.nseg * passes, bh);
     const bool split = g.a.nseg > 1;
     cudaError_t e = la::allow<la_main<DX, DZ>>((int)M::kBytes);
     if (e == cudaSuccess && (split || ends)) e = la::allow<la_states<DX, DZ>>((int)S::kBytes);
