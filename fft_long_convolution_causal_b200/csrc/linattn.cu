@@ -120,7 +120,7 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
     }
 }
 
-// grid (segments x passes, rows x heads); STATES: only the segments' own states.
+// One block a Place; STATES: only the segments' own states.
 // Warp w has rows 16 (w & 3) of scores and outputs, and every fourth 8-column
 // tile of theirs from w >> 2 on (tiles behind dz are left out); the state lives
 // in registers as accumulators (m-tiles w & 3, + 4), with a copy in shared
@@ -134,19 +134,20 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
     extern __shared__ __align__(16) float sm[];
     float *xs = sm, *ys = xs + kC * S::PX, *zs = ys + kC * S::PX, *ps = zs + kC * S::PZ, *ss = ps + kC * S::PP,
           *pw = ss + DX * S::PZ;
-    const int pass = pass_of(a);
-    const LaPass& p = a.p[pass];
-    const int tid = threadIdx.x, sg = segment_of(a), bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+    const Place at(a);
+    const LaPass& p = a.p[at.pass];
+    if (STATES && !p.s_out && at.ends(a)) return;
+    const int tid = threadIdx.x, bh = at.bh, b = bh / a.H, h = bh % a.H;
     const int lane = tid & 31, g = lane >> 2, t = lane & 3, warp = tid >> 5, mi = warp & 3, nj = warp >> 2;
     const bool rev = p.reverse;
-    const int64_t first = sg * a.seg, len = live_tokens(a, b);
-    const int64_t rows = min(a.seg, a.N - first);                   // output rows of this segment
+    const int64_t first = at.first, len = live_tokens(a, b);
+    const int64_t rows = at.tokens;                                 // output rows of this segment
     const int64_t live = max((int64_t)0, min(rows, len - first));   // of which read
     const float* x = (const float*)p.x + b * p.sx.batch + h * p.sx.head + first * p.sx.token;
     const float* y = (const float*)p.y + b * p.sy.batch + h * p.sy.head + first * p.sy.token;
     const float* z = (const float*)p.z + b * p.sz.batch + h * p.sz.head + first * p.sz.token;
     float* out = (float*)p.out + b * p.so.batch + h * p.so.head + first * p.so.token;
-    float* wseg = a.work + pass * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats;
+    float* wseg = a.work + at.state;
     for (int i = tid; i < kLaPowers; i += kThreads) pw[i] = a.pw[h * kLaPowers + i];
     // the state entering the segment
     if (STATES)
@@ -154,8 +155,8 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
     else
         after_previous();
     const uint32_t tiles = FULL ? ~0u : (1u << max(0, min(NT, (p.dz / 8 - nj + NG - 1) / NG))) - 1u;  // this warp's, those in front of dz
-    const float* s0 = STATES ? nullptr : p.carried ? wseg : p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
-    const bool trans = !p.carried && p.in_trans;
+    const float* s0 = STATES ? nullptr : at.split ? wseg : p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
+    const bool trans = !at.split && p.in_trans;
     float st[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
                             make_float2(acc[q][2 * r], acc[q][2 * r + 1]);
                 }
         }
-        if (STATES || ch + 1 < nch || (!p.carried && p.s_out)) {
+        if (STATES || ch + 1 < nch || (!at.split && p.s_out)) {
             // S <- a^L S + s_u sum_j a^(..) y_j^T z_j
             const float fl = pw[L];
 #pragma unroll
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
             }
         }
     }
-    float* so = STATES ? wseg : !p.carried && p.s_out ? p.s_out + (size_t)bh * p.dx * p.dz : nullptr;
+    float* so = STATES ? wseg : !at.split && p.s_out ? p.s_out + (size_t)bh * p.dx * p.dz : nullptr;
     if (so)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
     const LaPass& p = a.p[blockIdx.z];
     let_next_start();
     __shared__ float decay[kLaMaxSegments];  // over a segment; below zero: an empty one
-    const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, n = p.dx * p.dz;
+    const int bh = a.whole + blockIdx.y, b = bh / a.H, h = bh % a.H, n = p.dx * p.dz;
     const int64_t len = live_tokens(a, b);
     for (int k = threadIdx.x; k < a.nseg; k += kCarryThreads) {
         const int sg = p.reverse ? a.nseg - 1 - k : k;
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
     after_previous();
     const int e = 4 * (blockIdx.x * kCarryThreads + threadIdx.x);
     if (e >= n) return;
-    float* w = a.work + blockIdx.z * a.pass_floats + (size_t)bh * a.nseg * a.state_floats + e;
+    float* w = a.work + blockIdx.z * a.pass_floats + (size_t)blockIdx.y * a.nseg * a.state_floats + e;
     const int64_t step = (p.reverse ? -1 : 1) * (int64_t)a.state_floats;
     if (p.reverse) w += (a.nseg - 1) * a.state_floats;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -370,9 +371,9 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
     if (p.s_out) store4(p.s_out + (size_t)bh * n + e, s);
 }
 
-cudaError_t launch_carry(const Args& a, int bh, int passes, const double* lg, cudaStream_t s) {
+cudaError_t launch_carry(const Args& a, int rows, int passes, const double* lg, cudaStream_t s) {
     const unsigned blocks = (unsigned)((a.state_floats / 4 + kCarryThreads - 1) / kCarryThreads);
-    return launch<la_carry>(dim3(blocks, bh, passes), kCarryThreads, 0, s, true, a, lg);
+    return launch<la_carry>(dim3(blocks, rows, passes), kCarryThreads, 0, s, true, a, lg);
 }
 
 template <int DX, int DZ, bool FULL>
@@ -381,9 +382,11 @@ cudaError_t run(const Args& a, int bh, int passes, bool states, cudaStream_t s) 
     constexpr int bytes = S::kFloats * (int)sizeof(float);
     cudaError_t e = states ? allow<la_f32<DX, DZ, true, FULL>>(bytes) : allow<la_f32<DX, DZ, false, FULL>>(bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(a.nseg * passes, bh);
-    return states ? launch<la_f32<DX, DZ, true, FULL>>(grid, S::kThreads, bytes, s, false, a)
-                  : launch<la_f32<DX, DZ, false, FULL>>(grid, S::kThreads, bytes, s, a.nseg > 1, a);
+    const int split = (bh - a.whole) * a.nseg * passes;
+    Args g = a;
+    g.first = states ? a.whole * passes : 0;
+    return states ? launch<la_f32<DX, DZ, true, FULL>>(split, S::kThreads, bytes, s, false, g)
+                  : launch<la_f32<DX, DZ, false, FULL>>(a.whole * passes + split, S::kThreads, bytes, s, split > 0, g);
 }
 
 cudaError_t launch_f32(const Args& a, int dx, int dz, int bh, int passes, bool states, cudaStream_t s) {
@@ -500,22 +503,32 @@ int64_t slots_of(const fftconv_linattn_s& p, int passes) {
     return (int64_t)p.sms * (dx <= 64 && dz <= 64 ? 2 : 1);
 }
 
-// Segments the token axis is cut into.  In units of one chunk's time, a CTA
-// costs its chunks and about 1.5 to start; more than one segment adds the pass
-// over the segments' own states (two tensors of four: about 0.6 a chunk) and
-// the launch that joins them.
-int segments(const fftconv_linattn_s& p, int B, int64_t N, int passes) {
-    const int64_t chunks = (N + chunk_of(p) - 1) / chunk_of(p), ctas = (int64_t)B * p.H * passes;
-    const int64_t slots = slots_of(p, passes);
-    int best = 1;
-    double least = 0.0;
-    for (int n = 1; n <= kLaMaxSegments && n <= chunks && (n == 1 || ctas * n <= kLaMaxWaves * slots); ++n) {
-        const int64_t per = (chunks + n - 1) / n, waves = (ctas * n + slots - 1) / slots;
-        if (n > 1 && (chunks + per - 1) / per != n) continue;  // an empty segment
-        const double cost = waves * (per + 1.5) + (n > 1 ? waves * (0.6 * per + 1.0) + 3.0 : 0.0);
-        if (n == 1 || cost < least) {
-            best = n;
-            least = cost;
+// How a call is cut: rows (b, h) in front that run whole, and the segments that
+// the token axis of the others is cut into.  In units of one chunk's time, a CTA
+// costs its chunks and about 1.5 to start; segments add the pass over their own
+// states (two tensors of four: about 0.6 a chunk) and the launch that joins them.
+// Rows run whole as long as they fill the GPU; segments spread what is left over
+// it, or everything where there are few rows.
+struct Cut {
+    int whole, nseg;
+};
+Cut cut_of(const fftconv_linattn_s& p, int B, int64_t N, int passes) {
+    const int64_t chunks = (N + chunk_of(p) - 1) / chunk_of(p), rows = (int64_t)B * p.H, slots = slots_of(p, passes);
+    const int64_t full = rows * passes / slots * slots / passes;  // rows in whole waves
+    auto waves = [&](int64_t ctas) { return (double)((ctas + slots - 1) / slots); };
+    Cut best{(int)rows, 1};
+    double least = waves(rows * passes) * (chunks + 1.5);
+    for (int64_t n = 2; n <= kLaMaxSegments && n <= chunks; ++n) {
+        const int64_t per = (chunks + n - 1) / n;
+        if ((chunks + per - 1) / per != n) continue;  // an empty segment
+        for (int64_t whole : {(int64_t)0, full}) {
+            const int64_t ctas = (rows - whole) * passes * n;
+            if (ctas == 0 || ctas > kLaMaxWaves * slots) continue;
+            const double cost = waves(whole * passes) * (chunks + 1.5) + waves(ctas) * (per + 1.5 + 0.6 * per + 1.0) + 3.0;
+            if (cost < least) {
+                best = {(int)whole, (int)n};
+                least = cost;
+            }
         }
     }
     return best;
@@ -537,28 +550,30 @@ cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t 
     la::Args a;
     a.H = p.H;
     a.passes = c.passes;
-    a.nseg = segments(p, c.B, c.N, c.passes);
+    const int bh = c.B * p.H;
+    const Cut cut = cut_of(p, c.B, c.N, c.passes);
+    a.whole = cut.whole;
+    a.nseg = cut.nseg;
+    a.first = 0;
     a.seg = (chunks + a.nseg - 1) / a.nseg * chunk;
     a.N = c.N;
     a.lengths = c.lengths;
     a.pw = p.d_pow;
     a.work = c.work;
     a.state_floats = (size_t)p.dk * p.dv;
-    a.pass_floats = (size_t)c.B * p.H * a.nseg * a.state_floats;
+    a.pass_floats = (size_t)(bh - a.whole) * a.nseg * a.state_floats;
     bool ends = false;
     for (int i = 0; i < c.passes; ++i) {
         a.p[i] = c.pass[i];
-        a.p[i].carried = a.nseg > 1;
         ends = ends || a.p[i].s_out;
     }
     int dx, dz;
     padded(p, c.passes, &dx, &dz);
     if (tc) return la::launch_tc(a, dx, dz, c.B, c.passes, ends, p, s);
-    const int bh = c.B * p.H;
     cudaError_t e = cudaSuccess;
-    if (a.nseg > 1) {
+    if (bh > a.whole) {
         e = la::launch_f32(a, dx, dz, bh, c.passes, true, s);
-        if (e == cudaSuccess) e = la::launch_carry(a, bh, c.passes, p.d_log, s);
+        if (e == cudaSuccess) e = la::launch_carry(a, bh - a.whole, c.passes, p.d_log, s);
     }
     return e == cudaSuccess ? la::launch_f32(a, dx, dz, bh, c.passes, false, s) : e;
 }

@@ -11,18 +11,37 @@ namespace la {
 
 struct Args {
     LaPass p[kLaMaxPasses];
-    int H, nseg, passes;
+    int H, passes;
+    int whole, nseg;            // rows (b, h) in front that run unsplit, segments of each of the others
+    int first;                  // index of the launch's block 0 among all blocks
     int64_t N, seg;             // tokens, tokens a segment
     const int32_t* lengths;
     const float* pw;            // [H][kLaPowers]
-    float* work;                // [pass][bh][nseg][dk * dv]: segment states
+    float* work;                // [pass][split row][nseg][dk * dv]: segment states
     size_t pass_floats, state_floats;
 };
 
-// Block x runs pass x mod passes of segment x / passes: the passes of one (row, head) run side by side and find each
-// other's tensors in L2.
-__device__ __forceinline__ int pass_of(const Args& a) { return a.passes == 1 ? 0 : (int)blockIdx.x % a.passes; }
-__device__ __forceinline__ int segment_of(const Args& a) { return a.passes == 1 ? (int)blockIdx.x : (int)blockIdx.x / a.passes; }
+// What a block works on.  Blocks run over the unsplit rows, then over the segments of the others, the passes of one
+// row side by side: they find each other's tensors in L2.
+struct Place {
+    int pass, bh, sg;
+    bool split;
+    int64_t first, tokens;  // of the segment
+    size_t state;           // offset of its state in the workspace, in floats
+    __device__ __forceinline__ explicit Place(const Args& a) {
+        const int i = (int)blockIdx.x + a.first, r = i / a.passes;
+        pass = i - r * a.passes;
+        split = r >= a.whole;
+        const int s = r - a.whole;
+        bh = split ? a.whole + s / a.nseg : r;
+        sg = split ? s % a.nseg : 0;
+        first = sg * a.seg;
+        tokens = split ? min(a.seg, a.N - first) : a.N;
+        state = pass * a.pass_floats + (split ? (size_t)s * a.state_floats : 0);
+    }
+    // the pass's last segment, whose own state only a final state needs
+    __device__ __forceinline__ bool ends(const Args& a) const { return sg == (a.p[pass].reverse ? 0 : a.nseg - 1); }
+};
 
 __device__ __forceinline__ int64_t live_tokens(const Args& a, int b) {
     if (!a.lengths) return a.N;
@@ -66,7 +85,7 @@ cudaError_t launch(dim3 grid, int threads, size_t bytes, cudaStream_t s, bool ea
 }
 
 // Joins the segments' own states.
-cudaError_t launch_carry(const Args& a, int bh, int passes, const double* lg, cudaStream_t s);
+cudaError_t launch_carry(const Args& a, int rows, int passes, const double* lg, cudaStream_t s);
 // The whole call on tcgen05 (bf16); ends: a pass returns its final states.
 cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool ends, const fftconv_linattn_s& p,
                       cudaStream_t s);

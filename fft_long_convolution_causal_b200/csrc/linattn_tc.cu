@@ -153,9 +153,9 @@ struct Span {
     int64_t first, rows, live;  // first token of the segment, its tokens, of which live
     int nch;
     bool rev;
-    __device__ __forceinline__ Span(const la::Args& a, const LaPass& p, int sg, int b) {
-        first = sg * a.seg;
-        rows = min(a.seg, a.N - first);
+    __device__ __forceinline__ Span(const la::Args& a, const LaPass& p, const la::Place& at, int b) {
+        first = at.first;
+        rows = at.tokens;
         live = max((int64_t)0, min(rows, la::live_tokens(a, b) - first));
         nch = (int)((live + kC - 1) / kC);
         rev = p.reverse;
@@ -170,13 +170,13 @@ struct Copier {
     const Args& g;
     const LaPass& p;
     const Span& sp;
-    int b, h;
+    int pass, b, h;
     const Waiter& wait;
     // Tile `what` (0 y, 1 x, 2 z) of chunk n to dst, the use-th copy there, once the one before was left; false: a wait
     // gave up.
     __device__ __forceinline__ bool operator()(int what, int blocks, int n, uint32_t dst, const uint64_t& full,
                                                const uint64_t& empty, int use) const {
-        const int lane = threadIdx.x & 31, pass = la::pass_of(g.a);
+        const int lane = threadIdx.x & 31;
         if (use > 0 && !wait.all(empty, (uint32_t)(use - 1) & 1u)) return false;
         const int64_t t0 = sp.start(n);
         const int L = sp.tokens(n);
@@ -312,11 +312,11 @@ la_main(const __grid_constant__ Args g) {
     extern __shared__ __align__(1024) uint8_t smem[];
     MainTail& m = *reinterpret_cast<MainTail*>(smem + K::kOffTail);
     const la::Args& a = g.a;
-    const int pass = la::pass_of(a);
-    const LaPass& p = a.p[pass];
+    const la::Place at(a);
+    const LaPass& p = a.p[at.pass];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sg = la::segment_of(a), bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
-    const Span sp(a, p, sg, b);
+    const int bh = at.bh, b = bh / a.H, h = bh % a.H;
+    const Span sp(a, p, at, b);
     const bool rev = sp.rev;
     const int nch = sp.nch;
     const uint32_t sb = smem_u32(smem);
@@ -328,7 +328,7 @@ la_main(const __grid_constant__ Args g) {
     auto tile = [&](int n, int item) {
         return sb + (item == 1 ? 2 * K::kTX : item == 0 ? (uint32_t)(n & 1) * K::kTX : 3 * K::kTX + (uint32_t)(n & 1) * K::kTZ);
     };
-    const Copier copy{g, p, sp, b, h, wait};
+    const Copier copy{g, p, sp, at.pass, b, h, wait};
     auto load = [&](int n, int item) {
         if (n >= nch) return true;
         // z's place is free once the outputs staged there have left (this warp's own bulk copy)
@@ -343,7 +343,7 @@ la_main(const __grid_constant__ Args g) {
     auto store = [&](int n) {
         if (!wait.all(m.staged[n & 1], (uint32_t)(n >> 1) & 1u)) return false;
         if (lane == 0) {
-            const Source& so = g.src[g.out[pass]];
+            const Source& so = g.src[g.out[at.pass]];
             const int tk = (int)(sp.first + sp.start(n));
             const int c1 = so.at(1, tk, h, b), c2 = so.at(2, tk, h, b), c3 = so.at(3, tk, h, b);
 #pragma unroll 1
@@ -478,13 +478,11 @@ la_main(const __grid_constant__ Args g) {
         const int d = 32 * quarter + lane;
         const bool mine = 32 * quarter < DX;  // this warp's lanes hold rows of the state
         const uint32_t ts = tl + K::kST;
-        const float* s0 = p.carried ? a.work + pass * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats
-                          : p.s_in    ? p.s_in + (size_t)bh * p.dx * p.dz
-                                      : nullptr;
+        const float* s0 = at.split ? a.work + at.state : p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
         la::after_previous();  // the states entering the segments
         if (mine) {
 #pragma unroll 1
-            for (int n0 = 0; n0 < DZ; n0 += 32) state_in(ts, s0, !p.carried && p.in_trans, p, d, n0);
+            for (int n0 = 0; n0 < DZ; n0 += 32) state_in(ts, s0, !at.split && p.in_trans, p, d, n0);
             um::wait_st();
         }
         uint32_t o[DZ / 2];  // a row of O in bf16
@@ -660,12 +658,12 @@ la_states(const __grid_constant__ Args g) {
     extern __shared__ __align__(1024) uint8_t smem[];
     StatesTail& m = *reinterpret_cast<StatesTail*>(smem + K::kOffTail);
     const la::Args& a = g.a;
-    const int pass = la::pass_of(a);
-    const LaPass& p = a.p[pass];
-    if (!p.carried && !p.s_out) return;
+    const la::Place at(a);
+    const LaPass& p = a.p[at.pass];
+    if (!p.s_out && (!at.split || at.ends(a))) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sg = la::segment_of(a), bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
-    const Span sp(a, p, sg, b);
+    const int bh = at.bh, b = bh / a.H, h = bh % a.H;
+    const Span sp(a, p, at, b);
     const int nch = sp.nch;
     const uint32_t sb = smem_u32(smem);
     const Waiter wait{&m.abort, g.limit};
@@ -738,7 +736,7 @@ la_states(const __grid_constant__ Args g) {
         }
         drain(m.drain, &m.abort);
     } else if (warp == kCopyWarp) {
-        const Copier copy{g, p, sp, b, h, wait};
+        const Copier copy{g, p, sp, at.pass, b, h, wait};
         int made = 0;
 #pragma unroll 1
         for (; made < 2 * nch; ++made) {
@@ -772,10 +770,8 @@ la_states(const __grid_constant__ Args g) {
         const int d = 32 * quarter + lane;
         const bool mine = 32 * quarter < DX;
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16), ts = tl + K::kST;
-        const bool last = a.nseg == 1;  // the whole row: its final state, from the initial one
-        float* out = (last ? p.s_out + (size_t)bh * p.dx * p.dz
-                           : a.work + pass * a.pass_floats + ((size_t)bh * a.nseg + sg) * a.state_floats) +
-                     (size_t)d * p.dz;
+        const bool last = !at.split;  // the whole row: its final state, from the initial one
+        float* out = (last ? p.s_out + (size_t)bh * p.dx * p.dz : a.work + at.state) + (size_t)d * p.dz;
         const float* s0 = last && p.s_in ? p.s_in + (size_t)bh * p.dx * p.dz : nullptr;
         if (mine) {
 #pragma unroll 1
@@ -892,22 +888,23 @@ void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int 
 }
 
 template <int DX, int DZ>
-cudaError_t run(const Args& g, int bh, int passes, bool ends, const double* lg, cudaStream_t s) {
+cudaError_t run(Args& g, int bh, int passes, bool ends, const double* lg, cudaStream_t s) {
     using M = Main<DX, DZ>;
     using S = States<DX, DZ>;
-    const dim3 grid(g.a.nseg * passes, bh);
-    const bool split = g.a.nseg > 1;
+    const int whole = g.a.whole * passes, split = (bh - g.a.whole) * g.a.nseg * passes;
     cudaError_t e = la::allow<la_main<DX, DZ>>((int)M::kBytes);
     if (e == cudaSuccess && (split || ends)) e = la::allow<la_states<DX, DZ>>((int)S::kBytes);
     if (e == cudaSuccess && split) {
-        e = la::launch<la_states<DX, DZ>>(grid, S::kThreads, S::kBytes, s, false, g);
-        if (e == cudaSuccess) e = la::launch_carry(g.a, bh, passes, lg, s);
+        g.a.first = whole;
+        e = la::launch<la_states<DX, DZ>>(split, S::kThreads, S::kBytes, s, false, g);
+        if (e == cudaSuccess) e = la::launch_carry(g.a, bh - g.a.whole, passes, lg, s);
+        g.a.first = 0;
     }
-    if (e == cudaSuccess) e = la::launch<la_main<DX, DZ>>(grid, M::kThreads, M::kBytes, s, split, g);
+    if (e == cudaSuccess) e = la::launch<la_main<DX, DZ>>(whole + split, M::kThreads, M::kBytes, s, split > 0, g);
     // The outputs' kernel keeps its state for the outputs alone: final states that a caller asks for come from the
     // states' kernel, which sums them in fp32 (beside the outputs, but written after them: a caller may update its
     // states in place).
-    if (e == cudaSuccess && !split && ends) e = la::launch<la_states<DX, DZ>>(grid, S::kThreads, S::kBytes, s, true, g);
+    if (e == cudaSuccess && whole && ends) e = la::launch<la_states<DX, DZ>>(whole, S::kThreads, S::kBytes, s, true, g);
     return e;
 }
 

@@ -49,7 +49,6 @@ struct LaPass {
     float* s_out;                     // or NULL
     int in_trans;                     // s_in holds [dz][dx]
     float s_p, s_i, s_u;
-    int carried;                      // the states entering the segments are in the workspace
 };
 
 constexpr int kLaChunk = 64;      // tokens a step of the fp32 kernel

@@ -131,7 +131,7 @@ fftconv_status fftconv_linattn_fwd(const fftconv_linattn* p, const fftconv_linat
     c.passes = 1;
     c.B = a->B, c.H = p->H, c.N = a->N, c.lengths = a->lengths, c.work = (float*)workspace;
     c.pass[0] = {a->q, a->k, a->v, a->o, a->sq, a->sk, a->sv, a->so, p->dk, p->dv, 0,
-                 a->state_in, a->state_out, 0, scale, scale, 1.f, 0};
+                 a->state_in, a->state_out, 0, scale, scale, 1.f};
     return status_of(fftc::launch_la(*p, c, (cudaStream_t)stream));
 }
 
@@ -155,11 +155,11 @@ fftconv_status fftconv_linattn_bwd(const fftconv_linattn* p, const fftconv_linat
     c.passes = 3;
     c.B = a->B, c.H = p->H, c.N = a->N, c.lengths = a->lengths, c.work = (float*)workspace;
     c.pass[0] = {a->d_o, a->v, a->k, a->dq, a->sdo, a->sv, a->sk, a->sdq, p->dv, p->dk, 0,
-                 a->state_in, nullptr, 1, scale, scale, 1.f, 0};
+                 a->state_in, nullptr, 1, scale, scale, 1.f};
     c.pass[1] = {a->v, a->d_o, a->q, a->dk, a->sv, a->sdo, a->sq, a->sdk, p->dv, p->dk, 1,
-                 a->d_state, nullptr, 1, scale, 1.f, scale, 0};
+                 a->d_state, nullptr, 1, scale, 1.f, scale};
     c.pass[2] = {a->k, a->q, a->d_o, a->dv, a->sk, a->sq, a->sdo, a->sdv, p->dk, p->dv, 1,
-                 a->d_state, a->d_state_in, 0, scale, 1.f, scale, 0};
+                 a->d_state, a->d_state_in, 0, scale, 1.f, scale};
     return status_of(fftc::launch_la(*p, c, (cudaStream_t)stream));
 }
 
