@@ -466,9 +466,9 @@ la_main(const __grid_constant__ Args g) {
         for (; i <= 3 * nch && ok; ++i) ok = load_next(i);
         if (ok && nch) ok = store(nch - 1);
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        if (!ok || *wait.abort) {  // the last two chunks' copies may be in flight
-            const int n = (i + 2) / 3;
-            for (int c = n > 1 ? n - 1 : 0; c <= n && c < nch; ++c) {
+        if (!ok || *wait.abort) {  // copies of the last chunks may be in flight
+            const int n = (i - 1) / 3;
+            for (int c = n > 1 ? n - 1 : 0; c <= n + 1 && c < nch; ++c) {
                 um::mbar_wait(smem_u32(&m.zfull[c & 1]), (uint32_t)(c >> 1) & 1u, kLanding);
                 um::mbar_wait(smem_u32(&m.xy[c & 1]), (uint32_t)(c >> 1) & 1u, kLanding);
             }

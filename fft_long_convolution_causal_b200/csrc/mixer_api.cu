@@ -121,7 +121,7 @@ fftconv_status fftconv_linattn_fwd(const fftconv_linattn* p, const fftconv_linat
         return FFTCONV_ERR_INVALID_ARG;
     const int es = esize(p->dtype);
     if (!tokens_ok(a->q, a->sq, es) || !tokens_ok(a->k, a->sk, es) || !tokens_ok(a->v, a->sv, es) ||
-        !tokens_ok(a->o, a->so, es) || !distinct(a->so, a->B, p->H, a->N))
+        !tokens_ok(a->o, a->so, es) || !distinct(a->so, a->B, p->H, a->N) || a->o == a->q || a->o == a->k || a->o == a->v)
         return FFTCONV_ERR_INVALID_ARG;
     if (!aligned4(a->lengths) || !aligned16(a->state_in) || !aligned16(a->state_out) || !aligned16(workspace) ||
         (!workspace && fftconv_linattn_workspace_bytes(p, 0)))
@@ -146,6 +146,10 @@ fftconv_status fftconv_linattn_bwd(const fftconv_linattn* p, const fftconv_linat
         !tokens_ok(a->dv, a->sdv, es) || !distinct(a->sdq, a->B, p->H, a->N) || !distinct(a->sdk, a->B, p->H, a->N) ||
         !distinct(a->sdv, a->B, p->H, a->N))
         return FFTCONV_ERR_INVALID_ARG;
+    const void* in[4] = {a->d_o, a->q, a->k, a->v};
+    for (const void* x : in)
+        if (a->dq == x || a->dk == x || a->dv == x) return FFTCONV_ERR_INVALID_ARG;
+    if (a->dq == a->dk || a->dk == a->dv || a->dq == a->dv) return FFTCONV_ERR_INVALID_ARG;
     if (!aligned4(a->lengths) || !aligned16(a->state_in) || !aligned16(a->d_state) || !aligned16(a->d_state_in) ||
         !aligned16(workspace) || (!workspace && fftconv_linattn_workspace_bytes(p, 1)) ||
         (a->d_state_in && (a->d_state_in == a->d_state || a->d_state_in == a->state_in)))
@@ -262,7 +266,8 @@ fftconv_status fftconv_rotary_apply(const fftconv_rotary* p, const fftconv_rotar
     };
     if ((a->x == a->y && !same(a->sx, a->sy)) || (a->H2 && a->x2 == a->y2 && !same(a->sx2, a->sy2)))
         return FFTCONV_ERR_INVALID_ARG;
-    if ((double)a->B * (double)a->N * p->dim > 2147483647.0 * 256.0) return FFTCONV_ERR_UNSUPPORTED;  // one grid
+    if ((double)a->B * (double)a->N * p->dim > 2147483647.0 * 256.0 || (int64_t)a->H + a->H2 > 65535)
+        return FFTCONV_ERR_UNSUPPORTED;  // one grid
     const fftc::RotaryView v[2] = {
         {a->x, a->y, a->H, a->sx.batch, a->sx.head, a->sx.token, a->sy.batch, a->sy.head, a->sy.token},
         {a->x2, a->y2, a->H2, a->sx2.batch, a->sx2.head, a->sx2.token, a->sy2.batch, a->sy2.head, a->sy2.token}};

@@ -489,9 +489,12 @@ typedef struct {
  * q, k: [B][H][N][dk], v, o: [B][H][N][dv] of the plan's dtype; the state S
  * [dk][dv] in fp32, S_{-1} = state_in or zero.  dk and dv are multiples of 8
  * in [8, FFTCONV_LINATTN_MAX_DIM].  log_decay is a host array of H values
- * <= 0 (minus infinity: only the token itself), constants of the plan.  bf16
- * products accumulate in fp32; the scores and the state's copy read by q are
- * rounded to bf16 once, the state itself is not.
+ * <= 0 (minus infinity: only the token itself), constants of the plan.  bf16:
+ * products accumulate in fp32; the scores and the copy of the state that q
+ * reads are rounded to bf16 once, the state itself is not (the keys added to it
+ * are split into two or three bf16 terms).  fp32: every operand is split into
+ * two tf32 terms, results are those of fp32 arithmetic to a few units in the
+ * last place of the sums.  An infinity gives NaN there.
  * FFTCONV_ERR_UNSUPPORTED for other dims or B H > 65535.
  */
 #define FFTCONV_LINATTN_MAX_DIM 128
@@ -506,7 +509,7 @@ typedef struct {
     int B;
     int64_t N;
     double scale;
-    const void *q, *k, *v;
+    const void *q, *k, *v;   /* outputs overlap neither inputs nor each other                    */
     fftconv_strides sq, sk, sv;
     const int32_t* lengths;  /* [B] on the device or NULL: tokens of each row, clamped to [0, N]  */
     const float* state_in;   /* [B][H][dk][dv] or NULL                                            */

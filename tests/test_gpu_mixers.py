@@ -181,6 +181,127 @@ def test_linattn_backward(B, H, N, dk, dv, layout, state, dtype):
     assert plan.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linattn_rows_whole_and_split(dtype):
+    """A few rows more than fill the GPU: most run whole, the rest in segments."""
+    g, dt = gen(50), TORCH[dtype]
+    B, H, N, d = 50, 3, 1500, 128
+    q, k, v, do = (tokens(g, B, H, N, d, dt, "bnhd") for _ in range(4))
+    lg = decays(H, "slow")
+    plan = mixers().LinearAttentionPlan(B, H, N, d, d, lg, dtype=dtype)
+    s0, ds = normal(g, B, H, d, d), normal(g, B, H, d, d)
+    o, s1 = plan.fwd(q, k, v, state=s0, final_state=True)
+    got = plan.bwd(do, q, k, v, state=s0, dstate=ds)
+    for b in (0, 31, 48, 49):  # rows of either kind
+        one = [t[b:b + 1] for t in (q, k, v)]
+        want = linattn(*one, lg, plan.scale, s0[b:b + 1])
+        big = linattn(*absolutes(one), lg, plan.scale, s0[b:b + 1].abs())
+        check(o[b:b + 1], want[0], big[0], dtype, N, d, "o")
+        check(s1[b:b + 1], want[1], big[1], "f32", N, d, "state")
+        compare_gradients({n: t[b:b + 1] for n, t in got.items()}, (*one, s0[b:b + 1]), do[b:b + 1], ds[b:b + 1], lg,
+                          plan.scale, None, dtype, N)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linattn_one_tensor_for_all_and_one_token_for_all(dtype):
+    """q, k and v the same memory; a token repeated by a stride of zero; the same memory with two strides."""
+    g, dt = gen(51), TORCH[dtype]
+    B, H, N, d = 2, 3, 300, 64
+    x = tokens(g, B, H, N, d, dt, "bnhd")
+    one = normal(g, B, H, 1, d, dtype=dt).expand(B, H, N, d)
+    heads = x[:, :1].expand(B, H, N, d)
+    lg = decays(H)
+    plan = mixers().LinearAttentionPlan(B, H, N, d, d, lg, dtype=dtype)
+    for q, k, v in ((x, x, x), (one, x, one), (x, heads, x), (heads, x, heads)):
+        o, s = plan.fwd(q, k, v, final_state=True)
+        want, big = linattn(q, k, v, lg, plan.scale), linattn(*absolutes((q, k, v)), lg, plan.scale)
+        check(o, want[0], big[0], dtype, N, d, "o")
+        check(s, want[1], big[1], "f32", N, d, "state")
+        got = plan.bwd(x, q, k, v)
+        compare_gradients(got, (q, k, v, None), x, None, lg, plan.scale, None, dtype, N)
+
+
+def test_linattn_far_strides():
+    """Tokens 2^25 elements apart: offsets past 32 bits, in elements and in bytes."""
+    N, d, far = 140, 64, 1 << 25
+    buf = torch.empty(N * far, dtype=torch.bfloat16, device="cuda")
+    g = gen(52)
+    base = normal(g, 1, 1, N, d, dtype=torch.bfloat16)
+    views = [buf.as_strided((1, 1, N, d), (0, 0, far, 1), 64 * i) for i in range(4)]
+    for t in views[:3]:
+        t.copy_(base)
+    plan = mixers().LinearAttentionPlan(1, 1, N, d, d, [-0.01])
+    plan.fwd(*views[:3], o=views[3])
+    assert torch.equal(views[3], plan.fwd(base, base, base))
+    turn = mixers().RotaryPlan(d)
+    pos = torch.arange(N, device="cuda")
+    turn.apply(views[0], positions=pos, inplace=True)
+    assert torch.equal(views[0], turn.apply(base, positions=pos))
+
+
+def test_linattn_no_decay_and_full_decay():
+    """a = 1 over thousands of tokens, and a = 0: o_t = scale (q_t . k_t) v_t."""
+    g = gen(53)
+    B, H, N, d = 1, 2, 5000, 64
+    for dtype in ("bf16", "f32"):
+        q, k, v = (tokens(g, B, H, N, d, TORCH[dtype], "bhnd") for _ in range(3))
+        plan = mixers().LinearAttentionPlan(B, H, N, d, d, [0.0, -math.inf], dtype=dtype)
+        o, s = plan.fwd(q, k, v, final_state=True)
+        want, big = linattn(q, k, v, [0.0, -math.inf], plan.scale), linattn(*absolutes((q, k, v)), [0.0, -math.inf],
+                                                                           plan.scale)
+        check(o, want[0], big[0], dtype, N, d, "o")
+        check(s, want[1], big[1], "f32", N, d, "state")
+
+
+def test_linattn_wait_that_runs_out():
+    """No probe allowed: the call gives up, says so once, and the plan works again afterwards."""
+    g = gen(54)
+    for B, H, N, d in ((1, 2, 1000, 128), (2, 8, 700, 64)):
+        q, k, v = (tokens(g, B, H, N, d, torch.bfloat16, "bnhd") for _ in range(3))
+        plan = mixers().LinearAttentionPlan(B, H, N, d, d, decays(H, "slow"))
+        want = plan.fwd(q, k, v, final_state=True)
+        assert plan.device_status() == 0
+        plan.set_wait_limit(0)
+        plan.fwd(q, k, v, final_state=True)
+        assert plan.device_status() == 6 and plan.device_status() == 0
+        plan.set_wait_limit(65536)
+        got = plan.fwd(q, k, v, final_state=True)
+        assert plan.device_status() == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_linattn_state_in_place_and_streams_at_once():
+    """The final states may replace the initial ones; two streams use one plan at the same time."""
+    import ctypes
+    g = gen(55)
+    B, H, N, d = 40, 4, 256, 64  # one segment: the states' kernel runs beside the outputs'
+    m = mixers()
+    plan = m.LinearAttentionPlan(B, H, N, d, d, decays(H, "slow"))
+    q, k, v = (tokens(g, B, H, N, d, torch.bfloat16, "bnhd") for _ in range(3))
+    s0 = normal(g, B, H, d, d)
+    o, s1 = plan.fwd(q, k, v, state=s0, final_state=True)
+    for _ in range(5):
+        st, out = s0.clone(), torch.empty_like(v)
+        shape = (B, H, N, d)
+        a = m._FWD.pack(m._FWD.size, B, N, plan.scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        *plan._view(q, "q", shape), *plan._view(k, "k", shape), *plan._view(v, "v", shape), 0,
+                        st.data_ptr(), out.data_ptr(), *plan._view(out, "o", shape), st.data_ptr())
+        assert plan.lib.fftconv_linattn_fwd(plan._handle, a, plan._workspace(0).data_ptr(), plan._stream(None)) == 0
+        assert torch.equal(out, o) and torch.equal(st, s1)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        for s in side:
+            with torch.cuda.stream(s):
+                outs.append((plan.fwd(q, k, v, state=s0, final_state=True), plan.bwd(v, q, k, v, state=s0)))
+    torch.cuda.synchronize()
+    first = plan.bwd(v, q, k, v, state=s0)
+    for (a, b), grads in outs:
+        assert torch.equal(a, o) and torch.equal(b, s1)
+        assert all(torch.equal(grads[n], first[n]) for n in first)
+
+
 def test_linattn_backward_against_differences():
     """The operator is linear in each of q, k, v and the state: a central difference with step 1 is exact but for rounding."""
     g = gen(5)
@@ -599,6 +720,8 @@ def test_refusals_on_the_device():
         with pytest.raises(binding.FFTConvError) as e:
             plan.fwd(t, x, x)
         assert e.value.status == 1
+    with pytest.raises(binding.FFTConvError):  # an output that is an input
+        plan.fwd(x, x.clone(), x.clone(), o=x)
     with pytest.raises(binding.FFTConvError):  # an output shared by the heads
         plan.fwd(x, x, x, o=x[:, :1].expand(2, 3, 64, 64))
     with pytest.raises(ValueError):
