@@ -10,8 +10,12 @@
 // 16 bytes (or single elements where rows are not 16-byte aligned).  The weight
 // gradient is summed over the rows a block walks in registers, then over blocks
 // by a second kernel in a fixed order: repeated calls agree bit for bit.
+// 32768 x 768 bf16: forward 22.9 us (4.4 TB/s of x and y), backward 35.3 us
+// (4.3 TB/s of dy, x and dx), the launches' ramps included; 49152 x 64 fp32
+// forward 9.4 us, 17 x 2708 both ways 31 us, which is the host's time.
 #include <cuda_bf16.h>
 
+#include "linattn.cuh"
 #include "mixer.h"
 #include "pairs.cuh"
 
@@ -109,7 +113,7 @@ norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias
 }
 
 // The backward pass holds two rows of weight-gradient sums, a row and the next one's loads in registers: 12 warps of
-// up to 170 registers an SM (at 128 registers and 16 warps it spilled and took 98 us where it takes XX).
+// up to 170 registers an SM (at 128 registers and 16 warps it spilled, and 32768 x 768 took 98 us instead of 29).
 constexpr int kBwdThreads = 384;
 
 // Blocks blockIdx.x of group blockIdx.y walk the group's rows, the next row's loads in flight while a row is worked on;
@@ -194,6 +198,7 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __re
         }
         if (kAhead) row = next;
     }
+    la::let_next_start();
     // over the block's rows, then out
     float* out = part + ((int64_t)g * gridDim.x + blockIdx.x) * 2 * C;
     if constexpr (kRows > 1) {
@@ -239,6 +244,7 @@ __global__ void __launch_bounds__(1024) norm_reduce(const float* __restrict__ pa
     __shared__ float2 red[32][32];
     const int l = threadIdx.x % 32, c = blockIdx.x * 32 + l, k0 = threadIdx.x / 32, g = blockIdx.y;
     float2 s = make_float2(0.f, 0.f);
+    la::after_previous();
     if (c < C)
 #pragma unroll 4
         for (int k = k0; k < blocks; k += 32) {
@@ -374,8 +380,8 @@ cudaError_t launch_norm_bwd(const fftconv_norm_s& p, int64_t rows, const void* d
     cudaError_t e = p.dtype == FFTCONV_BF16 ? ln::pick<__nv_bfloat16>(p.C, ln::BwdPick{a, s})
                                             : ln::pick<float>(p.C, ln::BwdPick{a, s});
     if (e != cudaSuccess) return e;
-    ln::norm_reduce<<<dim3((p.C + 31) / 32, p.groups), 1024, 0, s>>>(work, dw, db, a.blocks, p.C);
-    return cudaGetLastError();
+    return la::launch<ln::norm_reduce>(dim3((p.C + 31) / 32, p.groups), 1024, 0, s, true, (const float*)work, dw, db,
+                                       a.blocks, p.C);
 }
 
 }  // namespace fftc

@@ -36,7 +36,7 @@ struct Two {
 };
 __device__ __forceinline__ Two split(float x) {
     Two r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r.hi) : "f"(x));
+    r.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to nearest, ties away (a NaN stays one in the second part)
     r.lo = __float_as_uint(x - __uint_as_float(r.hi));
     return r;
 }
@@ -121,11 +121,15 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
 }
 
 // One block a Place; STATES: only the segments' own states.
-// Warp w has rows 16 (w & 3) of scores and outputs, and every fourth 8-column
+// Warp w has rows 16 (w & 3) of scores and outputs, and every kGroups-th 8-column
 // tile of theirs from w >> 2 on (tiles behind dz are left out); the state lives
 // in registers as accumulators (m-tiles w & 3, + 4), with a copy in shared
-// memory for the outputs.  16 warps of 4 tiles or fewer: with 8 warps of twice
-// the tiles the issue slots stood at 54%.
+// memory for the outputs.  Two CTAs of 8 warps an SM at 64 x 64, one of 16 above.
+// Bound by issue: a product of 16 x 8 x 8 comes with ten instructions (its
+// operands' loads and splits, its share of the sums), issued in 53% of the slots,
+// and the tensor pipe is busy 42% of the time.  24 rows x 4096 at 64 x 64 take
+// 117 us (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 110 us; one product
+// of fp32 multiplications took 242 and 363.
 template <int DX, int DZ, bool STATES, bool FULL>
 __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCtas)) la_f32(const __grid_constant__ Args a) {
     using S = Shape<DX, DZ>;

@@ -1,5 +1,5 @@
-// linattn.cuh -- what the linear-attention kernels share: the argument block of
-// a call and the length of a row.
+// linattn.cuh -- what the linear-attention kernels share (the argument block of a
+// call, the length of a row, a block's place), and the launches that the mixers' kernels use.
 #pragma once
 
 #include <atomic>

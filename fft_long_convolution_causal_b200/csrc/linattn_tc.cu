@@ -240,8 +240,7 @@ __device__ __forceinline__ void split_y(uint32_t tile, uint32_t lo, uint32_t lo_
 }
 
 // One thread of a converged warp.  The issuing warp runs its loop as a whole, so that descriptors stay in uniform
-// registers, and only the products themselves are elected: issued from a branch on the lane, each product of
-// 64 cycles took 99.
+// registers, and only the products themselves are elected (gradients of 4 x 16 x 4096 x 128: 210 -> 203 us).
 __device__ __forceinline__ bool elect() {
     uint32_t r;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));

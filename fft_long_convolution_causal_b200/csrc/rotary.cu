@@ -9,7 +9,9 @@
 // cosine in fp32.
 //
 // Bound by memory (each element read and written once).  A thread owns some
-// pairs of one token, computes their sines once and walks a range of heads.
+// pairs of one token, computes their sines once and walks a range of heads, the
+// next heads' loads in flight: 4 x 4096 tokens x 32 heads x 128 in bf16 take
+// 48.5 us, 5.5 TB/s (75 us without loads ahead and packed arithmetic).
 #include <cuda_bf16.h>
 
 #include "mixer.h"

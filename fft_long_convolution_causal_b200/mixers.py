@@ -329,7 +329,8 @@ class LayerNormPlan(_Mixer):
             if y is None:
                 y = torch.empty_like(x)
             if statistics:
-                mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=self.device).unbind(0)
+                mean = torch.empty(rows, dtype=torch.float32, device=self.device)
+                rstd = torch.empty_like(mean)
         _check(self.lib.fftconv_norm_fwd(self._handle, rows, x.data_ptr(), weight.data_ptr(), bias.data_ptr(),
                                          y.data_ptr(), _data(mean), _data(rstd), self._stream(stream)),
                "fftconv_norm_fwd")
@@ -345,7 +346,8 @@ class LayerNormPlan(_Mixer):
         self._need(rstd, "rstd", (rows,), torch.float32)
         with self._on(stream):
             dx = torch.empty_like(x)
-            dw, db = torch.empty((2, self.groups, self.C), dtype=torch.float32, device=self.device).unbind(0)
+            dw = torch.empty((self.groups, self.C), dtype=torch.float32, device=self.device)
+            db = torch.empty_like(dw)
             ws = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         _check(self.lib.fftconv_norm_bwd(self._handle, rows, dy.data_ptr(), x.data_ptr(), weight.data_ptr(),
                                          mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(),
