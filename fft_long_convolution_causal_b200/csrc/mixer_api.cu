@@ -117,7 +117,7 @@ size_t fftconv_linattn_workspace_bytes(const fftconv_linattn* p, int backward) {
 fftconv_status fftconv_linattn_fwd(const fftconv_linattn* p, const fftconv_linattn_args* a, void* workspace,
                                    void* stream) {
     if (!p || !a || a->size != sizeof(*a) || a->B < 1 || a->B > p->B || a->N < 1 || a->N > p->N ||
-        !isfinite(a->scale) || !on_device(p->device))
+        !isfinite((float)a->scale) || !on_device(p->device))
         return FFTCONV_ERR_INVALID_ARG;
     const int es = esize(p->dtype);
     if (!tokens_ok(a->q, a->sq, es) || !tokens_ok(a->k, a->sk, es) || !tokens_ok(a->v, a->sv, es) ||
@@ -138,7 +138,7 @@ fftconv_status fftconv_linattn_fwd(const fftconv_linattn* p, const fftconv_linat
 fftconv_status fftconv_linattn_bwd(const fftconv_linattn* p, const fftconv_linattn_bwd_args* a, void* workspace,
                                    void* stream) {
     if (!p || !a || a->size != sizeof(*a) || a->B < 1 || a->B > p->B || a->N < 1 || a->N > p->N ||
-        !isfinite(a->scale) || !on_device(p->device))
+        !isfinite((float)a->scale) || !on_device(p->device))
         return FFTCONV_ERR_INVALID_ARG;
     const int es = esize(p->dtype);
     if (!tokens_ok(a->d_o, a->sdo, es) || !tokens_ok(a->q, a->sq, es) || !tokens_ok(a->k, a->sk, es) ||
@@ -168,7 +168,7 @@ fftconv_status fftconv_linattn_bwd(const fftconv_linattn* p, const fftconv_linat
 }
 
 fftconv_status fftconv_linattn_step(const fftconv_linattn* p, const fftconv_linattn_step_args* a, void* stream) {
-    if (!p || !a || a->size != sizeof(*a) || a->B < 1 || a->B > p->B || a->slots_n < 1 || !isfinite(a->scale) ||
+    if (!p || !a || a->size != sizeof(*a) || a->B < 1 || a->B > p->B || a->slots_n < 1 || !isfinite((float)a->scale) ||
         !a->q || !a->k || !a->v || !a->o || !a->state || !aligned16(a->state) || !aligned4(a->slots) ||
         (!a->slots && a->slots_n < a->B) || !distinct(a->so, a->B, p->H, 1) || !on_device(p->device))
         return FFTCONV_ERR_INVALID_ARG;
@@ -266,6 +266,7 @@ fftconv_status fftconv_rotary_apply(const fftconv_rotary* p, const fftconv_rotar
     };
     if ((a->x == a->y && !same(a->sx, a->sy)) || (a->H2 && a->x2 == a->y2 && !same(a->sx2, a->sy2)))
         return FFTCONV_ERR_INVALID_ARG;
+    if (a->H2 && (a->y == a->y2 || a->y == a->x2 || a->y2 == a->x)) return FFTCONV_ERR_INVALID_ARG;  // turned twice
     if ((double)a->B * (double)a->N * p->dim > 2147483647.0 * 256.0 || (int64_t)a->H + a->H2 > 65535)
         return FFTCONV_ERR_UNSUPPORTED;  // one grid
     const fftc::RotaryView v[2] = {

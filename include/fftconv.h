@@ -494,7 +494,10 @@ typedef struct {
  * reads are rounded to bf16 once, the state itself is not (the keys added to it
  * are split into two or three bf16 terms).  fp32: every operand is split into
  * two tf32 terms, results are those of fp32 arithmetic to a few units in the
- * last place of the sums.  An infinity gives NaN there.
+ * last place of the sums.  An infinity gives NaN there.  Tokens are taken in
+ * chunks (of 128 in bf16, 64 in fp32, from the first): a NaN or an infinity in v
+ * (backward: in q, k or d_o) reaches every output of its chunk, the earlier
+ * tokens' too; what lies behind a row's length is not read.
  * FFTCONV_ERR_UNSUPPORTED for other dims or B H > 65535.
  */
 #define FFTCONV_LINATTN_MAX_DIM 128
@@ -614,7 +617,7 @@ typedef struct {
     int64_t position_stride;         /* between rows                                              */
     int inverse;             /* the rotation by the negated angle, times m: the gradient         */
     const void *x, *x2;      /* [B][H][N][dim], strides any multiple of an element                */
-    void *y, *y2;            /* may be x, x2 with the same strides                                */
+    void *y, *y2;            /* may be x, x2 with the same strides; not the other's memory        */
     fftconv_strides sx, sx2, sy, sy2;
 } fftconv_rotary_args;
 

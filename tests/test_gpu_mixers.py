@@ -746,3 +746,38 @@ def test_refusals_on_the_device():
             norm.fwd(rows, torch.ones(3, 64, device="cuda"), torch.zeros(3, 64, device="cuda"))
     with pytest.raises(ValueError):
         norm.fwd(y, torch.ones(64, device="cuda"), torch.zeros(64, device="cuda"))
+
+
+def test_refusals_of_scales_and_of_one_tensor_turned_twice():
+    m = mixers()
+    from fft_long_convolution_causal_b200 import binding
+    x = torch.zeros(2, 3, 64, 64, dtype=torch.bfloat16, device="cuda")
+    plan = m.LinearAttentionPlan(2, 3, 64, 64, 64, decays(3), scale=1e39)  # finite, but not in fp32
+    with pytest.raises(binding.FFTConvError):
+        plan.fwd(x, x, x)
+    with pytest.raises(binding.FFTConvError):
+        plan.bwd(x, x, x, x)
+    with pytest.raises(binding.FFTConvError):
+        plan.step(x[:, :, 0], x[:, :, 0], x[:, :, 0], torch.zeros(2, 3, 64, 64, device="cuda"))
+    turn, at = m.RotaryPlan(64), torch.arange(64, device="cuda")
+    with pytest.raises(binding.FFTConvError):
+        turn.apply(x, x, positions=at, inplace=True)
+    a, b = turn.apply(x, x, positions=at)  # to two outputs
+    assert a.data_ptr() != b.data_ptr()
+
+
+def test_nonfinite_values_stay_in_their_row_and_behind_their_chunk():
+    """A NaN in v reaches its own row and head from its chunk on, nothing else."""
+    m = mixers()
+    for dtype, chunk in (("bf16", 128), ("f32", 64)):
+        t = torch.bfloat16 if dtype == "bf16" else torch.float32
+        g = torch.Generator().manual_seed(5)
+        q, k, v = (torch.randn(2, 2, 400, 64, generator=g).to(t).cuda() for _ in range(3))
+        plan = m.LinearAttentionPlan(2, 2, 400, 64, 64, decays(2), dtype=dtype)
+        clean = plan.fwd(q, k, v)
+        at = chunk + 7
+        v[1, 0, at] = float("nan")
+        o = plan.fwd(q, k, v)
+        assert torch.equal(o[0], clean[0]) and torch.equal(o[1, 1], clean[1, 1])
+        assert torch.equal(o[1, 0, :chunk], clean[1, 0, :chunk])
+        assert torch.isnan(o[1, 0, at:]).all()
