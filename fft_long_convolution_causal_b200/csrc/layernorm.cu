@@ -7,7 +7,11 @@
 //
 // Bound by memory.  A row is read once into registers (mean first, then the sum
 // of centred squares: no cancellation) by TPR threads, each holding E pieces of
-// 16 bytes (or single elements where rows are not 16-byte aligned).  The weight
+// 16 bytes.  Where C is not a multiple of a piece (OFF), a row starts up to a piece
+// behind a 16-byte boundary: pieces lie on the boundaries all the same, the two
+// at the row's ends are read and written by elements, and a thread walks rows in
+// steps that keep its columns, with their weights in registers.  38668 x 557 bf16
+// both ways: 318 us with one element a piece, 115 us so.  The weight
 // gradient is summed over the rows a block walks in registers, then over blocks
 // by a second kernel in a fixed order: repeated calls agree bit for bit.
 // 32768 x 768 bf16: forward 22.9 us (4.4 TB/s of x and y), backward 35.3 us
@@ -22,89 +26,185 @@
 namespace fftc {
 namespace ln {
 
-// threads of a block: rows on several warps have one row a block
-template <int TPR, int N>
-__host__ __device__ constexpr int block_threads() {
-    return TPR > 32 ? TPR : N;
-}
-
-// sum over the TPR threads of a row
+// rows a block: as many as its threads hold; the backward pass has 384 threads (up to 170 registers, see there)
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v) {
+constexpr int kFwdRows = TPR > 32 ? 1 : 256 / TPR;
+template <int TPR, int W>
+constexpr int kBwdRows = TPR > 128 ? 1 : TPR == 128 ? (W > 24 ? 2 : 3) : 384 / TPR;
+
+// Sums over the TPR threads of row `sub` of a block.  Rows on several warps meet in shared memory, in buffer `buf`:
+// two in turn, so that a buffer is written again only behind the barrier of the other.
+template <int TPR, int ROWS>
+__device__ __forceinline__ float2 row_sums(float2 v, int sub, int buf) {
 #pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
     if constexpr (TPR > 32) {
-        __shared__ float part[TPR / 32];
-        __syncthreads();  // the previous sum has been read
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = 0.f;
+        __shared__ float2 part[2][ROWS][TPR / 32];
+        if ((threadIdx.x & 31) == 0) part[buf][sub][threadIdx.x % TPR / 32] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(sub + 1), "r"(TPR) : "memory");
+        v = both(0.f);
 #pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) v += part[i];
+        for (int i = 0; i < TPR / 32; ++i) v = add2(v, part[buf][sub][i]);
     }
     return v;
 }
+template <int TPR, int ROWS>
+__device__ __forceinline__ float row_sum(float v, int sub, int buf) {
+    if constexpr (TPR > 32) {
+        return row_sums<TPR, ROWS>(make_float2(v, 0.f), sub, buf).x;
+    } else {
+#pragma unroll
+        for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+}
 
-template <typename T, int V, int TPR, int E>
-__global__ void __launch_bounds__((block_threads<TPR, 256>()))
+// two elements, stored together
+template <typename T>
+struct alignas(2 * sizeof(T)) Two {
+    T x, y;
+    __device__ __forceinline__ explicit Two(float2 v) : x(T(v.x)), y(T(v.y)) {}
+};
+
+// The pieces of a thread: columns first(i) .. first(i) + V - 1 of its rows.
+template <typename T, int V, int TPR, bool OFF>
+struct Columns {
+    using P = Piece<T, V>;
+    int lane, off, C;  // off: elements between the 16-byte boundary and the row
+    __device__ __forceinline__ int first(int i) const { return (lane + i * TPR) * V - (OFF ? off : 0); }
+    __device__ __forceinline__ bool any(int i) const { return first(i) < C; }
+    __device__ __forceinline__ bool inside(int i) const { return !OFF || (first(i) >= 0 && first(i) + V <= C); }
+    __device__ __forceinline__ bool has(int c) const { return (unsigned)c < (unsigned)C; }
+    // A piece at a row's end is loaded whole (its other elements are a neighbouring row's), but by elements at the end
+    // of the last row; trim() puts zeros in place of what is not the row's.
+    __device__ __forceinline__ void load(P& q, const T* row, int i, bool last) const {
+        const int c = first(i);
+        if (!OFF || !last || c + V <= C) {
+            q = *reinterpret_cast<const P*>(row + c);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P::kPairs; ++j)
+                q.set(j, make_float2(has(c + 2 * j) ? (float)row[c + 2 * j] : 0.f,
+                                     has(c + 2 * j + 1) ? (float)row[c + 2 * j + 1] : 0.f));
+        }
+    }
+    __device__ __forceinline__ void trim(P& q, int i) const {
+        if (inside(i)) return;
+        const int c = first(i);
+#pragma unroll
+        for (int j = 0; j < P::kPairs; ++j) {
+            const float2 v = q.get(j);
+            q.set(j, make_float2(has(c + 2 * j) ? v.x : 0.f, has(c + 2 * j + 1) ? v.y : 0.f));
+        }
+    }
+    // by pairs and elements at the row's ends
+    __device__ __forceinline__ void store(const P& q, T* row, int i) const {
+        const int c = first(i);
+        if (inside(i)) {
+            *reinterpret_cast<P*>(row + c) = q;
+        } else {
+#pragma unroll
+            for (int j = 0; j < P::kPairs; ++j) {
+                const int e = c + 2 * j;
+                const Two<T> v(q.get(j));
+                if (e >= 0 && e + 1 < C)
+                    *reinterpret_cast<Two<T>*>(row + e) = v;
+                else if (has(e))
+                    row[e] = v.x;
+                else if (has(e + 1))
+                    row[e + 1] = v.y;
+            }
+        }
+    }
+    __device__ __forceinline__ float2 weight(const float* w, int i, int j) const {
+        const int c = first(i) + 2 * j;
+        return make_float2(has(c) ? w[c] : 0.f, has(c + 1) ? w[c + 1] : 0.f);
+    }
+};
+template <int V, bool OFF>
+__device__ __forceinline__ int offset(int64_t row, int C) {
+    return OFF ? (int)((uint64_t)row * (uint64_t)C % V) : 0;
+}
+
+template <typename T, int V, int TPR, int E, bool OFF>
+__global__ void __launch_bounds__((TPR * kFwdRows<TPR>), (OFF && TPR <= 32 ? 2 : 0))
 norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias, T* y, float* __restrict__ mean,
-         float* __restrict__ rstd, int64_t rows, int C, int G, float eps) {
+         float* __restrict__ rstd, int64_t rows, int64_t step, int C, int G, float eps) {
     using P = Piece<T, V>;
     using W = Piece<float, V>;
-    constexpr int kRows = block_threads<TPR, 256>() / TPR;
-    const int lane = threadIdx.x % TPR, items = C / V;
-    const int64_t step = (int64_t)gridDim.x * kRows;
-    constexpr int NP = P::kPairs;
+    constexpr int kRows = kFwdRows<TPR>, NP = P::kPairs;
+    const int sub = threadIdx.x / TPR;
     const float inv = 1.f / (float)C;
+    int64_t r = (int64_t)blockIdx.x * kRows + sub;
+    if (r >= step) r = rows;  // OFF: past the last of a step's rows
+    const Columns<T, V, TPR, OFF> col{(int)(threadIdx.x % TPR), offset<V, OFF>(r, C), C};
     P p[E];
     auto fetch = [&](int64_t r) {
         if (r >= rows) return;
-        const P* xr = reinterpret_cast<const P*>(x + r * C);
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (lane + i * TPR < items) p[i] = xr[lane + i * TPR];
+            if (col.any(i)) col.load(p[i], x + r * C, i, r == rows - 1);
     };
-    int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     fetch(r);
+    float2 hw[OFF ? E : 1][NP], hb[OFF ? E : 1][NP];
+    if constexpr (OFF) {
+        const int64_t g = r < rows ? r % G : 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+#pragma unroll
+            for (int j = 0; j < NP; ++j) hw[i][j] = col.weight(w + g * C, i, j), hb[i][j] = col.weight(bias + g * C, i, j);
+    }
     for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += step, r += step) {
         const bool on = r < rows;
         float2 v[E][NP], s = both(0.f);
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (lane + i * TPR < items && on) {
+            if (col.any(i) && on) {
+                col.trim(p[i], i);
 #pragma unroll
                 for (int j = 0; j < NP; ++j) s = add2(s, v[i][j] = p[i].get(j));
             }
         fetch(r + step);  // in flight while this row is worked on
-        const float mu = row_sum<TPR>(s.x + s.y) * inv;
+        const float mu = row_sum<TPR, kRows>(s.x + s.y, sub, 0) * inv;
         s = both(0.f);
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (lane + i * TPR < items && on) {
+            if (col.any(i) && on) {
 #pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    v[i][j] = add2(v[i][j], make_float2(-mu, V > 1 ? -mu : 0.f));
-                    s = fma2(v[i][j], v[i][j], s);
+                for (int j = 0; j < NP; ++j) v[i][j] = add2(v[i][j], both(-mu));
+                if (!col.inside(i)) {
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        if (!col.has(col.first(i) + 2 * j)) v[i][j].x = 0.f;
+                        if (!col.has(col.first(i) + 2 * j + 1)) v[i][j].y = 0.f;
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < NP; ++j) s = fma2(v[i][j], v[i][j], s);
             }
-        const float rs = 1.f / sqrtf(row_sum<TPR>(s.x + s.y) * inv + eps);
+        const float rs = 1.f / sqrtf(row_sum<TPR, kRows>(s.x + s.y, sub, 1) * inv + eps);
         if (on) {
-            const int64_t g = G == 1 ? 0 : r % G;
+            const int64_t g = OFF || G == 1 ? 0 : r % G;
             const W* wr = reinterpret_cast<const W*>(w + g * C);
             const W* br = reinterpret_cast<const W*>(bias + g * C);
-            P* yr = reinterpret_cast<P*>(y + r * C);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = lane + i * TPR;
-                if (c < items) {
-                    const W wv = wr[c], bv = br[c];
+            for (int i = 0; i < E; ++i)
+                if (col.any(i)) {
                     P o;
+                    if constexpr (OFF) {
 #pragma unroll
-                    for (int j = 0; j < NP; ++j) o.set(j, fma2(mul2(v[i][j], both(rs)), wv.get(j), bv.get(j)));
-                    yr[c] = o;
+                        for (int j = 0; j < NP; ++j) o.set(j, fma2(mul2(v[i][j], both(rs)), hw[i][j], hb[i][j]));
+                    } else {
+                        const W wv = wr[col.lane + i * TPR], bv = br[col.lane + i * TPR];
+#pragma unroll
+                        for (int j = 0; j < NP; ++j) o.set(j, fma2(mul2(v[i][j], both(rs)), wv.get(j), bv.get(j)));
+                    }
+                    col.store(o, y + r * C, i);
                 }
-            }
-            if (lane == 0) {
+            if (col.lane == 0) {
                 if (mean) mean[r] = mu;
                 if (rstd) rstd[r] = rs;
             }
@@ -114,27 +214,49 @@ norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias
 
 // The backward pass holds two rows of weight-gradient sums, a row and the next one's loads in registers: 12 warps of
 // up to 170 registers an SM (at 128 registers and 16 warps it spilled, and 32768 x 768 took 98 us instead of 29).
-constexpr int kBwdThreads = 384;
-
 // Blocks blockIdx.x of group blockIdx.y walk the group's rows, the next row's loads in flight while a row is worked on;
 // partial sums of the weight gradients to part[(group * blocks + block)][2][C].
-template <typename T, int V, int TPR, int E>
-__global__ void __launch_bounds__((block_threads<TPR, kBwdThreads>()), 1)
+template <typename T, int V, int TPR, int E, bool OFF>
+__global__ void __launch_bounds__((TPR * kBwdRows<TPR, E * V>), 1)
 norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __restrict__ mean,
-         const float* __restrict__ rstd, T* dx, float* __restrict__ part, int64_t rows, int C, int G) {
+         const float* __restrict__ rstd, T* dx, float* __restrict__ part, int64_t rows, int64_t step, int C, int G) {
     using P = Piece<T, V>;
     using W = Piece<float, V>;
-    constexpr int kThreads = block_threads<TPR, kBwdThreads>(), kRows = kThreads / TPR;
-    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR, items = C / V, g = blockIdx.y;
-    const int64_t group_rows = rows / G, step = (int64_t)gridDim.x * kRows;
+    constexpr int kRows = kBwdRows<TPR, E * V>, kThreads = TPR * kRows, NP = P::kPairs;
+    const int sub = threadIdx.x / TPR, g = blockIdx.y;
+    const int64_t group_rows = rows / G;
     const float inv = 1.f / (float)C;
-    constexpr int NP = P::kPairs;
+    int64_t k = (int64_t)blockIdx.x * kRows + sub;
+    if (k >= step) k = group_rows;  // OFF: past the last of a step's rows
+    const Columns<T, V, TPR, OFF> col{(int)(threadIdx.x % TPR), offset<V, OFF>(k * G + g, C), C};
     float2 dw[E][NP], db[E][NP];
 #pragma unroll
     for (int i = 0; i < E; ++i)
 #pragma unroll
         for (int j = 0; j < NP; ++j) dw[i][j] = db[i][j] = both(0.f);
     const W* wr = reinterpret_cast<const W*>(w + (int64_t)g * C);
+    float2 hw[OFF ? E : 1][NP];
+    if constexpr (OFF) {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+#pragma unroll
+            for (int j = 0; j < NP; ++j) hw[i][j] = col.weight(w + (int64_t)g * C, i, j);
+    }
+    struct Weights {
+        float2 v[NP];
+    };
+    auto weights = [&](int i) {
+        Weights q;
+        if constexpr (OFF) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) q.v[j] = hw[i][j];
+        } else {
+            const W wv = wr[col.lane + i * TPR];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) q.v[j] = wv.get(j);
+        }
+        return q;
+    };
     struct Row {
         P x[E], d[E];
         float mu, rs;
@@ -142,22 +264,20 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __re
     auto fetch = [&](Row& q, int64_t k) {
         if (k >= group_rows) return;
         const int64_t r = k * G + g;
-        const P* xr = reinterpret_cast<const P*>(x + r * C);
-        const P* dr = reinterpret_cast<const P*>(dy + r * C);
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (lane + i * TPR < items) {
-                q.x[i] = xr[lane + i * TPR];
-                q.d[i] = dr[lane + i * TPR];
+            if (col.any(i)) {
+                col.load(q.x[i], x + r * C, i, r == rows - 1);
+                col.load(q.d[i], dy + r * C, i, r == rows - 1);
             }
         q.mu = mean[r];
         q.rs = rstd[r];
     };
     constexpr bool kAhead = E * V <= 24;  // where the registers allow it
     Row row;
-    if (kAhead) fetch(row, (int64_t)blockIdx.x * kRows + sub);
-    for (int64_t k0 = (int64_t)blockIdx.x * kRows; k0 < group_rows; k0 += step) {
-        const int64_t k = k0 + sub;
+    if (kAhead) fetch(row, k);
+    int buf = 0;
+    for (int64_t k0 = (int64_t)blockIdx.x * kRows; k0 < group_rows; k0 += step, k += step, buf ^= 1) {
         const bool on = k < group_rows;
         Row next;
         if (kAhead)
@@ -165,35 +285,37 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __re
         else
             fetch(row, k);
         float2 s1 = both(0.f), s2 = both(0.f);
-        const float2 rs = both(row.rs), shift = make_float2(-row.mu, V > 1 ? -row.mu : 0.f);
+        const float2 rs = both(row.rs), shift = both(-row.mu);
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (lane + i * TPR < items && on) {
-                const W wv = wr[lane + i * TPR];
+            if (col.any(i) && on) {
+                col.trim(row.x[i], i);
+                col.trim(row.d[i], i);
+                const Weights wv = weights(i);
 #pragma unroll
                 for (int j = 0; j < NP; ++j) {
-                    const float2 d = row.d[i].get(j), xh = mul2(add2(row.x[i].get(j), shift), rs), gv = mul2(d, wv.get(j));
+                    const float2 d = row.d[i].get(j), xh = mul2(add2(row.x[i].get(j), shift), rs), gv = mul2(d, wv.v[j]);
                     dw[i][j] = fma2(d, xh, dw[i][j]);
                     db[i][j] = add2(db[i][j], d);
                     s1 = add2(s1, gv);
                     s2 = fma2(gv, xh, s2);
                 }
             }
-        const float m1 = row_sum<TPR>(s1.x + s1.y) * inv, m2 = row_sum<TPR>(s2.x + s2.y) * inv;
+        const float2 m = row_sums<TPR, kRows>(make_float2(s1.x + s1.y, s2.x + s2.y), sub, buf);
+        const float m1 = m.x * inv, m2 = m.y * inv;
         if (on) {
-            P* o = reinterpret_cast<P*>(dx + (k * G + g) * C);
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                if (lane + i * TPR < items) {
-                    const W wv = wr[lane + i * TPR];
+                if (col.any(i)) {
+                    const Weights wv = weights(i);
                     P q;
 #pragma unroll
                     for (int j = 0; j < NP; ++j) {
                         const float2 xh = mul2(add2(row.x[i].get(j), shift), rs);
-                        const float2 c = fma2(row.d[i].get(j), wv.get(j), both(-m1));
+                        const float2 c = fma2(row.d[i].get(j), wv.v[j], both(-m1));
                         q.set(j, mul2(rs, fma2(xh, both(-m2), c)));
                     }
-                    o[lane + i * TPR] = q;
+                    col.store(q, dx + (k * G + g) * C, i);
                 }
         }
         if (kAhead) row = next;
@@ -211,30 +333,31 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __re
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float2 u = q ? db[i][j / 2] : dw[i][j / 2];
-                    red[sub][(i * V + j) * TPR + lane] = j & 1 ? u.y : u.x;
+                    const int c = col.first(i) + j;
+                    if (!OFF || col.has(c)) red[sub][OFF ? c : (i * V + j) * TPR + col.lane] = j & 1 ? u.y : u.x;
                 }
             __syncthreads();
-            for (int e = threadIdx.x; e < TPR * E * V; e += kThreads) {
-                const int l = e % TPR, j = e / TPR % V, i = e / TPR / V, c = l + i * TPR;
-                if (c < items) {
+            for (int e = threadIdx.x; e < (OFF ? C : TPR * E * V); e += kThreads) {
+                const int c = OFF ? e : (e % TPR + e / TPR / V * TPR) * V + e / TPR % V;
+                if (c < C) {
                     float v = 0.f;
 #pragma unroll
                     for (int k = 0; k < kRows; ++k) v += red[k][e];
-                    out[q * C + c * V + j] = v;
+                    out[q * C + c] = v;
                 }
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = lane + i * TPR;
-            if (c < items)
+        for (int i = 0; i < E; ++i)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    out[c * V + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
-                    out[C + c * V + j] = j & 1 ? db[i][j / 2].y : db[i][j / 2].x;
+            for (int j = 0; j < V; ++j) {
+                const int c = col.first(i) + j;
+                if (col.has(c)) {
+                    out[c] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+                    out[C + c] = j & 1 ? db[i][j / 2].y : db[i][j / 2].x;
                 }
-        }
+            }
     }
 }
 
@@ -279,82 +402,115 @@ struct BwdArgs {
     const void *dy, *x;
     const float *w, *mean, *rstd;
     void* dx;
-    float* part;
+    float *part, *dw, *db;
     int64_t rows;
     int C, G, blocks;
 };
 
-template <typename T, int V, int TPR, int E>
+int64_t common_multiple(int64_t a, int64_t b) {
+    int64_t x = a, y = b;
+    while (y) {
+        const int64_t t = x % y;
+        x = y;
+        y = t;
+    }
+    return a / x * b;
+}
+
+template <typename T, int V, int TPR, int E, bool OFF>
 cudaError_t fwd(const FwdArgs& a, cudaStream_t s) {
-    constexpr int kThreads = block_threads<TPR, 256>(), kRows = kThreads / TPR;
+    constexpr int kRows = kFwdRows<TPR>, kThreads = TPR * kRows;
     // the blocks that the SMs hold at once, each walking rows
     static const int held = [] {
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_fwd<T, V, TPR, E>, kThreads, 0) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_fwd<T, V, TPR, E, OFF>, kThreads, 0) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
         }
         return n > 0 ? n : 1;
     }();
-    const int64_t blocks = (a.rows + kRows - 1) / kRows, most = (int64_t)a.sms * held;
-    norm_fwd<T, V, TPR, E><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, s>>>(
-        (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd, a.rows, a.C, a.G, a.eps);
+    const int64_t all = (a.rows + kRows - 1) / kRows * kRows, most = (int64_t)a.sms * held * kRows;
+    int64_t step = all < most ? all : most;
+    if (OFF && step < a.rows) {  // a thread's rows have one offset and one weight row
+        const int64_t unit = common_multiple(V, a.G);
+        step = step > unit ? step / unit * unit : unit;
+    }
+    const int64_t units = step < all ? step : all;
+    norm_fwd<T, V, TPR, E, OFF><<<(unsigned)((units + kRows - 1) / kRows), kThreads, 0, s>>>(
+        (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd, a.rows, step, a.C, a.G, a.eps);
     return cudaGetLastError();
 }
-template <typename T, int V, int TPR, int E>
+template <typename T, int V, int TPR, int E, bool OFF>
 cudaError_t bwd(const BwdArgs& a, cudaStream_t s) {
-    norm_bwd<T, V, TPR, E><<<dim3(a.blocks, a.G), block_threads<TPR, kBwdThreads>(), 0, s>>>(
-        (const T*)a.dy, (const T*)a.x, a.w, a.mean, a.rstd, (T*)a.dx, a.part, a.rows, a.C, a.G);
-    return cudaGetLastError();
+    constexpr int kRows = kBwdRows<TPR, E * V>;
+    const int64_t group_rows = a.rows / a.G, all = (group_rows + kRows - 1) / kRows;
+    const int blocks = (int)(a.blocks < all ? a.blocks : all);
+    int64_t step = (int64_t)blocks * kRows;
+    if (OFF && step < group_rows) step = step / V * V;  // at least V: see bwd_blocks
+    norm_bwd<T, V, TPR, E, OFF><<<dim3(blocks, a.G), TPR * kRows, 0, s>>>(
+        (const T*)a.dy, (const T*)a.x, a.w, a.mean, a.rstd, (T*)a.dx, a.part, a.rows, step, a.C, a.G);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return la::launch<norm_reduce>(dim3((a.C + 31) / 32, a.G), 1024, 0, s, true, (const float*)a.part, a.dw, a.db, blocks,
+                                   a.C);
 }
 
 // threads and pieces a row, by its pieces: the fewest threads that hold a row in few registers
-template <typename T, int V, typename F>
-cudaError_t by_items(int items, F f) {
-    if constexpr (V > 1) {
-        if (items <= 8) return f.template operator()<T, V, 8, 1>();
-        if (items <= 16) return f.template operator()<T, V, 16, 1>();
-        if (items <= 32) return f.template operator()<T, V, 32, 1>();
-        if (items <= 64) return f.template operator()<T, V, 32, 2>();
-        if (items <= 96) return f.template operator()<T, V, 32, 3>();
-        if (items <= 128) return f.template operator()<T, V, 32, 4>();
-        if (items <= 256) return f.template operator()<T, V, 128, 2>();
-        if (items <= 512) return f.template operator()<T, V, 128, 4>();
-        if (items <= 1024) return f.template operator()<T, V, 512, 2>();
-        if (items <= 2048) return f.template operator()<T, V, 512, 4>();
-        return f.template operator()<T, V, 512, 8>();
-    } else {
-        if (items <= 256) return f.template operator()<T, 1, 32, 8>();
-        if (items <= 1024) return f.template operator()<T, 1, 128, 8>();
-        if (items <= 4096) return f.template operator()<T, 1, 512, 8>();
-        return f.template operator()<T, 1, 512, 32>();
+template <typename T, typename F>
+cudaError_t pick(int C, F f) {
+    constexpr int V = 16 / sizeof(T);
+    if (C % V == 0) {
+        const int items = C / V;
+        if (items <= 8) return f.template operator()<T, V, 8, 1, false>();
+        if (items <= 16) return f.template operator()<T, V, 16, 1, false>();
+        if (items <= 32) return f.template operator()<T, V, 32, 1, false>();
+        if (items <= 64) return f.template operator()<T, V, 32, 2, false>();
+        if (items <= 96) return f.template operator()<T, V, 32, 3, false>();
+        if (items <= 128) return f.template operator()<T, V, 32, 4, false>();
+        if (items <= 256) return f.template operator()<T, V, 128, 2, false>();
+        if (items <= 512) return f.template operator()<T, V, 128, 4, false>();
+        if (items <= 1024) return f.template operator()<T, V, 512, 2, false>();
+        if (items <= 2048) return f.template operator()<T, V, 512, 4, false>();
+        return f.template operator()<T, V, 512, 8, false>();
     }
+    const int items = (C + 2 * V - 2) / V;  // of the largest offset; the weights are in registers too
+    if (items <= 8) return f.template operator()<T, V, 8, 1, true>();
+    if (items <= 16) return f.template operator()<T, V, 8, 2, true>();
+    if (items <= 24) return f.template operator()<T, V, 8, 3, true>();
+    if (items <= 32) return f.template operator()<T, V, 16, 2, true>();
+    if (items <= 48) return f.template operator()<T, V, 16, 3, true>();
+    if (items <= 64) return f.template operator()<T, V, 32, 2, true>();
+    if (items <= 96) return f.template operator()<T, V, 32, 3, true>();
+    if (items <= 128) return f.template operator()<T, V, 128, 1, true>();
+    if (items <= 256) return f.template operator()<T, V, 128, 2, true>();
+    if (items <= 384) return f.template operator()<T, V, 128, 3, true>();
+    if (items <= 512) return f.template operator()<T, V, 512, 1, true>();
+    if (items <= 1024) return f.template operator()<T, V, 512, 2, true>();
+    if (items <= 1536) return f.template operator()<T, V, 512, 3, true>();
+    return f.template operator()<T, V, 512, V == 8 ? 5 : 9, true>();  // 16383 columns and an offset
 }
 struct FwdPick {
     const FwdArgs& a;
     cudaStream_t s;
-    template <typename T, int V, int TPR, int E>
+    template <typename T, int V, int TPR, int E, bool OFF>
     cudaError_t operator()() {
-        return fwd<T, V, TPR, E>(a, s);
+        return fwd<T, V, TPR, E, OFF>(a, s);
     }
 };
 struct BwdPick {
     const BwdArgs& a;
     cudaStream_t s;
-    template <typename T, int V, int TPR, int E>
+    template <typename T, int V, int TPR, int E, bool OFF>
     cudaError_t operator()() {
-        return bwd<T, V, TPR, E>(a, s);
+        return bwd<T, V, TPR, E, OFF>(a, s);
     }
 };
-template <typename T, typename F>
-cudaError_t pick(int C, F f) {
-    constexpr int V = 16 / sizeof(T);
-    return C % V == 0 ? by_items<T, V>(C / V, f) : by_items<T, 1>(C, f);
-}
 
-// blocks a group of the backward pass: one an SM in all, no more than rows
+// Blocks a group of the backward pass: at most one an SM in all, no more than rows; eight where rows start at different offsets,
+// so that a step of rows can be a multiple of the offsets' period.
 inline int bwd_blocks(const fftconv_norm_s& p, int64_t rows) {
-    int64_t n = ((int64_t)p.sms + p.groups - 1) / p.groups;
+    int64_t n = p.sms / p.groups;
+    if (n < 8 && p.C % (p.dtype == FFTCONV_BF16 ? 8 : 4)) n = 8;
     const int64_t most = rows / p.groups;
     n = n < most ? n : most;
     return (int)(n < 1 ? 1 : n);
@@ -376,12 +532,9 @@ size_t norm_workspace_bytes(const fftconv_norm_s& p) {
 cudaError_t launch_norm_bwd(const fftconv_norm_s& p, int64_t rows, const void* dy, const void* x, const float* w,
                             const float* mean, const float* rstd, void* dx, float* dw, float* db, float* work,
                             cudaStream_t s) {
-    const ln::BwdArgs a{dy, x, w, mean, rstd, dx, work, rows, p.C, p.groups, ln::bwd_blocks(p, rows)};
-    cudaError_t e = p.dtype == FFTCONV_BF16 ? ln::pick<__nv_bfloat16>(p.C, ln::BwdPick{a, s})
-                                            : ln::pick<float>(p.C, ln::BwdPick{a, s});
-    if (e != cudaSuccess) return e;
-    return la::launch<ln::norm_reduce>(dim3((p.C + 31) / 32, p.groups), 1024, 0, s, true, (const float*)work, dw, db,
-                                       a.blocks, p.C);
+    const ln::BwdArgs a{dy, x, w, mean, rstd, dx, work, dw, db, rows, p.C, p.groups, ln::bwd_blocks(p, rows)};
+    return p.dtype == FFTCONV_BF16 ? ln::pick<__nv_bfloat16>(p.C, ln::BwdPick{a, s})
+                                   : ln::pick<float>(p.C, ln::BwdPick{a, s});
 }
 
 }  // namespace fftc

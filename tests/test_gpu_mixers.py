@@ -781,3 +781,30 @@ def test_nonfinite_values_stay_in_their_row_and_behind_their_chunk():
         assert torch.equal(o[0], clean[0]) and torch.equal(o[1, 1], clean[1, 1])
         assert torch.equal(o[1, 0, :chunk], clean[1, 0, :chunk])
         assert torch.isnan(o[1, 0, at:]).all()
+
+
+UNALIGNED = [(1, 1, 1), (7, 3, 7), (39999, 21, 3), (4000, 13, 1000), (5000, 55, 1), (1776 * 3, 131, 1), (14 * 300, 557, 14),
+             (2000, 761, 1), (900, 762, 1), (12 * 75, 1021, 12), (601, 1018, 1), (333, 2042, 1), (23 * 20, 1541, 23),
+             (310, 3058, 1), (160, 8185, 1), (170, 8186, 1), (23 * 9, 5001, 23), (150, 16383, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,C,G", UNALIGNED)
+def test_layernorm_rows_off_16_bytes(rows, C, G, dtype):
+    """Rows that start anywhere in a 16-byte piece, walked in several steps, on one and on several warps."""
+    test_layernorm(rows, C, G, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layernorm_in_place_and_within_its_rows(dtype):
+    g, dt = gen(31), TORCH[dtype]
+    for rows, C in ((700, 37), (300, 557), (200, 768), (150, 2050)):
+        room = torch.full((rows * C + 64,), 7.0, dtype=dt, device="cuda")
+        x = normal(g, rows, C, dtype=dt)
+        w, b = 1 + 0.3 * normal(g, 1, C), normal(g, 1, C)
+        plan = mixers().LayerNormPlan(rows, C, dtype=dtype)
+        y = plan.fwd(x, w, b)
+        at = room[:rows * C].view(rows, C)
+        assert plan.fwd(x, w, b, y=at) is at and torch.equal(at, y) and (room[rows * C:] == 7).all()
+        z = x.clone()
+        assert torch.equal(plan.fwd(z, w, b, y=z), y)
