@@ -11,7 +11,7 @@
 // behind a 16-byte boundary: pieces lie on the boundaries all the same, the two
 // at the row's ends are read and written by elements, and a thread walks rows in
 // steps that keep its columns, with their weights in registers.  38668 x 557 bf16
-// both ways: 318 us with one element a piece, 115 us so.  The weight
+// both ways: 318 us with one element a piece, 108 us so.  The weight
 // gradient is summed over the rows a block walks in registers, then over blocks
 // by a second kernel in a fixed order: repeated calls agree bit for bit.
 // 32768 x 768 bf16: forward 22.9 us (4.4 TB/s of x and y), backward 35.3 us
@@ -130,7 +130,7 @@ __device__ __forceinline__ int offset(int64_t row, int C) {
 }
 
 template <typename T, int V, int TPR, int E, bool OFF>
-__global__ void __launch_bounds__((TPR * kFwdRows<TPR>), (OFF && TPR <= 32 ? 2 : 0))
+__global__ void __launch_bounds__((TPR * kFwdRows<TPR>), (OFF && TPR <= 32 ? (E < 3 ? 3 : 2) : 0))
 norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias, T* y, float* __restrict__ mean,
          float* __restrict__ rstd, int64_t rows, int64_t step, int C, int G, float eps) {
     using P = Piece<T, V>;
@@ -480,16 +480,17 @@ cudaError_t pick(int C, F f) {
     if (items <= 32) return f.template operator()<T, V, 16, 2, true>();
     if (items <= 48) return f.template operator()<T, V, 16, 3, true>();
     if (items <= 64) return f.template operator()<T, V, 32, 2, true>();
-    if (items <= 96) return f.template operator()<T, V, 32, 3, true>();
+    if (F::kThree && items <= 96) return f.template operator()<T, V, 32, 3, true>();
     if (items <= 128) return f.template operator()<T, V, 128, 1, true>();
     if (items <= 256) return f.template operator()<T, V, 128, 2, true>();
-    if (items <= 384) return f.template operator()<T, V, 128, 3, true>();
+    if (F::kThree && items <= 384) return f.template operator()<T, V, 128, 3, true>();
     if (items <= 512) return f.template operator()<T, V, 512, 1, true>();
     if (items <= 1024) return f.template operator()<T, V, 512, 2, true>();
     if (items <= 1536) return f.template operator()<T, V, 512, 3, true>();
     return f.template operator()<T, V, 512, V == 8 ? 5 : 9, true>();  // 16383 columns and an offset
 }
 struct FwdPick {
+    static constexpr bool kThree = false;  // registers for a third block an SM: 38668 x 557 bf16 54 -> 48 us
     const FwdArgs& a;
     cudaStream_t s;
     template <typename T, int V, int TPR, int E, bool OFF>
@@ -498,6 +499,7 @@ struct FwdPick {
     }
 };
 struct BwdPick {
+    static constexpr bool kThree = true;  // a row on one warp: 60 us, on four 80
     const BwdArgs& a;
     cudaStream_t s;
     template <typename T, int V, int TPR, int E, bool OFF>
