@@ -808,3 +808,25 @@ def test_layernorm_in_place_and_within_its_rows(dtype):
         assert plan.fwd(x, w, b, y=at) is at and torch.equal(at, y) and (room[rows * C:] == 7).all()
         z = x.clone()
         assert torch.equal(plan.fwd(z, w, b, y=z), y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dim,rot", [(8, 2), (8, 6), (16, 10), (16, 14)] + [(40, r) for r in range(2, 41, 2)]
+                         + [(128, 90), (128, 92), (128, 126), (256, 30), (256, 254)])
+def test_rotary_parts_of_a_head(dim, rot, layout, dtype):
+    """Rotated parts that end, or have their half, inside a 16-byte piece; in place the same, the rest as it was."""
+    if rot > 2:  # one pair has no scaled base
+        test_rotary(2, 9, 2, 17, dim, rot, layout, dtype)
+    g, dt = gen(rot), TORCH[dtype]
+    x = normal(g, 2, 9, 17, dim, dtype=dt)
+    if rot < dim:
+        x[..., rot], x[..., -1] = float("inf"), float("nan")
+    pos = torch.arange(17, device="cuda") + 5
+    plan = mixers().RotaryPlan(dim, rot_dim=rot, layout=layout, dtype=dtype)
+    y = plan.apply(x, positions=pos)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(y[..., rot:].view(bits), x[..., rot:].view(bits)) and torch.isfinite(y[..., :rot]).all()
+    z = x.clone()
+    plan.apply(z, positions=pos, inplace=True)
+    assert torch.equal(z.view(bits), y.view(bits))
