@@ -830,3 +830,9 @@ def test_rotary_parts_of_a_head(dim, rot, layout, dtype):
     z = x.clone()
     plan.apply(z, positions=pos, inplace=True)
     assert torch.equal(z.view(bits), y.view(bits))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layernorm_more_weight_rows_than_sms(dtype):
+    for rows, C, G in ((400, 64, 200), (600, 2048, 300), (1200, 67, 600)):
+        test_layernorm(rows, C, G, dtype)
