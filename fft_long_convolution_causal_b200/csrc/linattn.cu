@@ -128,7 +128,7 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
 // Bound by issue: a product of 16 x 8 x 8 comes with ten instructions (its
 // operands' loads and splits, its share of the sums), issued in 53% of the slots,
 // and the tensor pipe is busy 42% of the time.  24 rows x 4096 at 64 x 64 take
-// 117 us (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 110 us; one product
+// 114 us (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 110 us; one product
 // of fp32 multiplications took 242 and 363.
 template <int DX, int DZ, bool STATES, bool FULL>
 __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCtas)) la_f32(const __grid_constant__ Args a) {
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
         }
         if (STATES || ch + 1 < nch || (!at.split && p.s_out)) {
             // S <- a^L S + s_u sum_j a^(..) y_j^T z_j
+            constexpr int kSteps = FULL ? 2 : 1;  // into one u; with the conditions on tiles beside it, two spill
             const float fl = pw[L];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -286,22 +287,29 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st[m][q][e] *= fl;
 #pragma unroll 1
-            for (int k = 0; k < L; k += 8) {
-                float u[NT][4];
-                const float w0 = p.s_u * pw[rev ? k + t + 1 : max(L - 1 - k - t, 0)],
-                            w1 = p.s_u * pw[rev ? k + t + 5 : max(L - 5 - k - t, 0)];
-                Two fb[NT][2];
+            for (int k = 0; k < L; k += 8 * kSteps) {  // rows behind the length are zeros
+                float u[MT][NT][4];
 #pragma unroll
-                for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], zs, k, 8 * (nj + NG * q), g, t);
+                for (int s = 0; s < kSteps; ++s) {
+                    const int j = k + 8 * s + t;
+                    const float w0 = p.s_u * pw[rev ? j + 1 : max(L - 1 - j, 0)],
+                                w1 = p.s_u * pw[rev ? j + 5 : max(L - 5 - j, 0)];
+                    Two fb[NT][2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (!FULL && 16 * (mi + 4 * m) >= p.dx) break;
-                    const float* v = ys + (k + t) * S::PX + 16 * (mi + 4 * m) + g;
-                    Two fa[4];
-                    fa[0] = split(w0 * v[0]), fa[1] = split(w0 * v[8]);
-                    fa[2] = split(w1 * v[4 * S::PX]), fa[3] = split(w1 * v[4 * S::PX + 8]);
-                    mma3<true>(u, fa, fb, tiles);
-                    add(st[m], u, tiles);
+                    for (int q = 0; q < NT; ++q) frag_b<S::PZ>(fb[q], zs, k + 8 * s, 8 * (nj + NG * q), g, t);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        if (!FULL && 16 * (mi + 4 * m) >= p.dx) break;
+                        const float* v = ys + j * S::PX + 16 * (mi + 4 * m) + g;
+                        Two fa[4];
+                        fa[0] = split(w0 * v[0]), fa[1] = split(w0 * v[8]);
+                        fa[2] = split(w1 * v[4 * S::PX]), fa[3] = split(w1 * v[4 * S::PX + 8]);
+                        if (s == 0)
+                            mma3<true>(u[m], fa, fb, tiles);
+                        else
+                            mma3<false>(u[m], fa, fb, tiles);
+                        if (s + 1 == kSteps) add(st[m], u[m], tiles);
+                    }
                 }
             }
         }
