@@ -128,8 +128,8 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
 // Bound by issue: a product of 16 x 8 x 8 comes with ten instructions (its
 // operands' loads and splits, its share of the sums), issued in 53% of the slots,
 // and the tensor pipe is busy 42% of the time.  24 rows x 4096 at 64 x 64 take
-// 114 us (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 110 us; one product
-// of fp32 multiplications took 242 and 363.
+// 114 us (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 110 to 145 us
+// (as its lengths fall); fp32 multiplications without the tensor cores took 242 and 363.
 template <int DX, int DZ, bool STATES, bool FULL>
 __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCtas)) la_f32(const __grid_constant__ Args a) {
     using S = Shape<DX, DZ>;
