@@ -21,6 +21,7 @@
 
 #include "linattn.cuh"
 #include "mixer.h"
+#include "norm_rows.h"
 #include "pairs.cuh"
 
 namespace fftc {
@@ -69,20 +70,19 @@ struct alignas(2 * sizeof(T)) Two {
     __device__ __forceinline__ explicit Two(float2 v) : x(T(v.x)), y(T(v.y)) {}
 };
 
-// The pieces of a thread: columns first(i) .. first(i) + V - 1 of its rows.
+// A thread's pieces of rows in memory.
 template <typename T, int V, int TPR, bool OFF>
-struct Columns {
+struct Columns : Pieces<V, TPR, OFF> {
     using P = Piece<T, V>;
-    int lane, off, C;  // off: elements between the 16-byte boundary and the row
-    __device__ __forceinline__ int first(int i) const { return (lane + i * TPR) * V - (OFF ? off : 0); }
-    __device__ __forceinline__ bool any(int i) const { return first(i) < C; }
-    __device__ __forceinline__ bool inside(int i) const { return !OFF || (first(i) >= 0 && first(i) + V <= C); }
-    __device__ __forceinline__ bool has(int c) const { return (unsigned)c < (unsigned)C; }
-    // A piece at a row's end is loaded whole (its other elements are a neighbouring row's), but by elements at the end
-    // of the last row; trim() puts zeros in place of what is not the row's.
-    __device__ __forceinline__ void load(P& q, const T* row, int i, bool last) const {
+    using Pieces<V, TPR, OFF>::first, Pieces<V, TPR, OFF>::inside, Pieces<V, TPR, OFF>::has, Pieces<V, TPR, OFF>::C;
+    __device__ __forceinline__ Columns(int lane, int off, int C) : Pieces<V, TPR, OFF>{lane, off, C} {}
+    // A piece at a row's end is loaded whole (its other elements are a neighbouring row's), but by elements at the
+    // tensor's end; trim() puts zeros in place of what is not the row's.  In place, another block may be storing the
+    // neighbour's elements of such a piece meanwhile: whichever bytes come back for them, trim() drops them, and the
+    // row's own are written by this thread alone, later.
+    __device__ __forceinline__ void load(P& q, const T* row, int i, int end) const {
         const int c = first(i);
-        if (!OFF || !last || c + V <= C) {
+        if (this->whole(i, end)) {
             q = *reinterpret_cast<const P*>(row + c);
         } else {
 #pragma unroll
@@ -124,11 +124,6 @@ struct Columns {
         return make_float2(has(c) ? w[c] : 0.f, has(c + 1) ? w[c + 1] : 0.f);
     }
 };
-template <int V, bool OFF>
-__device__ __forceinline__ int offset(int64_t row, int C) {
-    return OFF ? (int)((uint64_t)row * (uint64_t)C % V) : 0;
-}
-
 template <typename T, int V, int TPR, int E, bool OFF>
 __global__ void __launch_bounds__((TPR * kFwdRows<TPR>), (OFF && TPR <= 32 ? (E < 3 ? 3 : 2) : 0))
 norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias, T* y, float* __restrict__ mean,
@@ -140,13 +135,13 @@ norm_fwd(const T* x, const float* __restrict__ w, const float* __restrict__ bias
     const float inv = 1.f / (float)C;
     int64_t r = (int64_t)blockIdx.x * kRows + sub;
     if (r >= step) r = rows;  // OFF: past the last of a step's rows
-    const Columns<T, V, TPR, OFF> col{(int)(threadIdx.x % TPR), offset<V, OFF>(r, C), C};
+    const Columns<T, V, TPR, OFF> col((int)(threadIdx.x % TPR), offset<V, OFF>(r, C), C);
     P p[E];
     auto fetch = [&](int64_t r) {
         if (r >= rows) return;
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            if (col.any(i)) col.load(p[i], x + r * C, i, r == rows - 1);
+            if (col.any(i)) col.load(p[i], x + r * C, i, to_end(r, rows, C));
     };
     fetch(r);
     float2 hw[OFF ? E : 1][NP], hb[OFF ? E : 1][NP];
@@ -228,7 +223,7 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __re
     const float inv = 1.f / (float)C;
     int64_t k = (int64_t)blockIdx.x * kRows + sub;
     if (k >= step) k = group_rows;  // OFF: past the last of a step's rows
-    const Columns<T, V, TPR, OFF> col{(int)(threadIdx.x % TPR), offset<V, OFF>(k * G + g, C), C};
+    const Columns<T, V, TPR, OFF> col((int)(threadIdx.x % TPR), offset<V, OFF>(k * G + g, C), C);
     float2 dw[E][NP], db[E][NP];
 #pragma unroll
     for (int i = 0; i < E; ++i)
@@ -267,8 +262,8 @@ norm_bwd(const T* dy, const T* x, const float* __restrict__ w, const float* __re
 #pragma unroll
         for (int i = 0; i < E; ++i)
             if (col.any(i)) {
-                col.load(q.x[i], x + r * C, i, r == rows - 1);
-                col.load(q.d[i], dy + r * C, i, r == rows - 1);
+                col.load(q.x[i], x + r * C, i, to_end(r, rows, C));
+                col.load(q.d[i], dy + r * C, i, to_end(r, rows, C));
             }
         q.mu = mean[r];
         q.rs = rstd[r];
