@@ -419,7 +419,7 @@ cudaError_t launch_f32(const Args& a, int dx, int dz, int bh, int passes, bool s
 constexpr int kStepThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kStepThreads)
-la_step(const LaStep c, int H, int dk, int dv, const float* __restrict__ pw) {
+la_step(const LaStep c, int H, int dk, int dv, const float2* __restrict__ decay) {
     __shared__ float sq[128], sk[128], sv[128];
     __shared__ float4 part[kStepThreads];
     const int h = blockIdx.x, tid = threadIdx.x;
@@ -449,7 +449,7 @@ la_step(const LaStep c, int H, int dk, int dv, const float* __restrict__ pw) {
         if (__syncthreads_or(before)) return;
         more = __syncthreads_or(after);
     }
-    const float a = pw[h * kLaPowers + 1];
+    const float2 a = decay[h * kLaPowers + 1];
     for (int b = b0; b < c.B; ++b) {
         if (b != b0 && c.slots[b] != slot) continue;
         __syncthreads();
@@ -467,8 +467,8 @@ la_step(const LaStep c, int H, int dk, int dv, const float* __restrict__ pw) {
                 const int d = grp + i * groups;
                 if (d < dk) {
                     const float k = sk[d], q = sq[d];
-                    s[i].x = fmaf(a, s[i].x, k * v.x), s[i].y = fmaf(a, s[i].y, k * v.y);
-                    s[i].z = fmaf(a, s[i].z, k * v.z), s[i].w = fmaf(a, s[i].w, k * v.w);
+                    s[i].x = decayed(a, s[i].x, k * v.x), s[i].y = decayed(a, s[i].y, k * v.y);
+                    s[i].z = decayed(a, s[i].z, k * v.z), s[i].w = decayed(a, s[i].w, k * v.w);
                     o.x = fmaf(q, s[i].x, o.x), o.y = fmaf(q, s[i].y, o.y);
                     o.z = fmaf(q, s[i].z, o.z), o.w = fmaf(q, s[i].w, o.w);
                 }
@@ -598,9 +598,9 @@ cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t 
 cudaError_t launch_la_step(const fftconv_linattn_s& p, const LaStep& c, cudaStream_t s) {
     const dim3 grid(p.H, c.B);
     if (p.dtype == FFTCONV_BF16)
-        la::la_step<__nv_bfloat16><<<grid, la::kStepThreads, 0, s>>>(c, p.H, p.dk, p.dv, p.d_pow);
+        la::la_step<__nv_bfloat16><<<grid, la::kStepThreads, 0, s>>>(c, p.H, p.dk, p.dv, p.d_decay);
     else
-        la::la_step<float><<<grid, la::kStepThreads, 0, s>>>(c, p.H, p.dk, p.dv, p.d_pow);
+        la::la_step<float><<<grid, la::kStepThreads, 0, s>>>(c, p.H, p.dk, p.dv, p.d_decay);
     return cudaGetLastError();
 }
 

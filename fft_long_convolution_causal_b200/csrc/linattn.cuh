@@ -49,6 +49,10 @@ __device__ __forceinline__ int64_t live_tokens(const Args& a, int b) {
     return n < 0 ? 0 : n > a.N ? a.N : n;
 }
 
+// a s + u for a decay a in two parts.  Rounded to fp32, a is off by up to 2^-25, always to the same side, and a state
+// that lives for n steps would drift by n times that (a decay nearer to one than that would not decay at all).
+__device__ __forceinline__ float decayed(float2 a, float s, float u) { return fmaf(a.x, s, fmaf(a.y, s, u)); }
+
 // The shared-memory limit of a kernel, set once a device (again at worst).
 template <auto kKernel>
 cudaError_t allow(int bytes) {

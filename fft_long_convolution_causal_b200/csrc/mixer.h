@@ -15,6 +15,7 @@ struct fftconv_linattn_s {
     void* block = nullptr;            // one allocation: the tables below and the status word
     const double* d_log = nullptr;    // [H] natural logarithm of the decay
     const float* d_pow = nullptr;     // [H][kLaPowers] a^n, n = 0, 1, ...
+    const float2* d_decay = nullptr;  // [H][kLaPowers] a^n in two parts, for what a state is multiplied by again and again
     int* d_err = nullptr;             // device status word
     uint32_t wait_limit = FFTCONV_DEFAULT_WAIT_PROBES;
 };

@@ -75,16 +75,24 @@ fftconv_status fftconv_linattn_plan_create(fftconv_linattn** out, int B, int H, 
     if (!p) return FFTCONV_ERR_OOM;
     p->B = B, p->H = H, p->N = N, p->dk = dk, p->dv = dv, p->dtype = dtype;
     current_device(&p->device, &p->sms);
-    // [H] logarithms, [H][kLaPowers] powers (computed in fp64), the status word
-    const size_t off_pow = (size_t)H * sizeof(double), off_err = off_pow + (size_t)H * fftc::kLaPowers * sizeof(float);
+    // [H] logarithms, [H][kLaPowers] powers (computed in fp64) rounded and in two parts, the status word
+    const size_t n = (size_t)H * fftc::kLaPowers, off_pow = (size_t)H * sizeof(double),
+                 off_decay = (off_pow + n * sizeof(float) + 7) / 8 * 8, off_err = off_decay + n * sizeof(float2);
     try {
         std::vector<unsigned char> host(off_err + 16, 0);
-        for (int h = 0; h < H; ++h) {
-            memcpy(&host[h * sizeof(double)], &log_decay[h], sizeof(double));
-            for (int n = 0; n < fftc::kLaPowers; ++n) {
-                const float a = n == 0 ? 1.f : (float)exp(log_decay[h] * n);
-                memcpy(&host[off_pow + ((size_t)h * fftc::kLaPowers + n) * sizeof(float)], &a, sizeof(float));
-            }
+        memcpy(&host[0], log_decay, off_pow);
+        for (size_t i = 0; i < n; ++i) {
+            const size_t h = i / fftc::kLaPowers, e = i % fftc::kLaPowers;
+            const double a = e == 0 ? 1.0 : exp(log_decay[h] * (double)e);
+            const float near = (float)a;
+            // The first part is rounded down, so that the second is positive, and the second never zero where that
+            // changes nothing: an infinite state then stays one (no infinity of the other sign, no 0 x infinity).
+            const float hi = near > a ? nextafterf(near, 0.f) : near;
+            float lo = (float)(a - hi);
+            if (hi >= 0x1p-100f) lo = fmaxf(lo, 0x1p-149f);
+            const float2 parts = make_float2(hi, lo);
+            memcpy(&host[off_pow + i * sizeof(float)], &near, sizeof(float));
+            memcpy(&host[off_decay + i * sizeof(float2)], &parts, sizeof(float2));
         }
         const fftconv_status st = upload(host.data(), host.size(), &p->block);
         if (st != FFTCONV_OK) {
@@ -97,6 +105,7 @@ fftconv_status fftconv_linattn_plan_create(fftconv_linattn** out, int B, int H, 
     }
     p->d_log = (const double*)p->block;
     p->d_pow = (const float*)((const unsigned char*)p->block + off_pow);
+    p->d_decay = (const float2*)((const unsigned char*)p->block + off_decay);
     p->d_err = (int*)((unsigned char*)p->block + off_err);
     *out = p;
     return FFTCONV_OK;

@@ -564,7 +564,11 @@ typedef struct {
 
 /* One token a row, the recurrent form.  A row whose slot is outside
  * [0, slots_n) is idle: zeros in o, no state touched.  Rows that name one slot
- * are taken in row order. */
+ * are taken in row order.  The decay is applied in two parts, so that a state
+ * follows it over thousands of tokens; each token rounds the state once.  (So
+ * where every k v lies on the state's fp32 grid, as bf16 products do once the
+ * state has grown 2^8 times theirs, a decay by less than 2^-24 a token is lost
+ * in that rounding.) */
 FFTCONV_API fftconv_status fftconv_linattn_step(const fftconv_linattn* plan, const fftconv_linattn_step_args* args,
                                                 void* stream);
 

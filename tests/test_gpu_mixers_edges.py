@@ -72,3 +72,56 @@ def test_layernorm_gradient_in_place(rows, C, dtype):
                                        plan._stream(None))
     assert status == 0
     assert all(torch.equal(s, t) for s, t in zip((vd, dw, db), want)) and around_is_nan(bd, dy.numel())
+
+
+# neither powers of two nor near them; the last two nearer to one than fp32 holds
+SLOW = [-0.0123, -3.35e-4, -1e-5, -4.1e-8, -2e-8]
+
+
+def recurrence(k, v, log_decay, state=None):
+    """S_t = a S_{t-1} + k_t^T v_t in 64 bits, token by token: the last state."""
+    B, H, N, dk = k.shape
+    a = torch.exp(torch.tensor(log_decay, dtype=torch.float64, device="cuda"))[:, None, None]
+    S = torch.zeros(B, H, dk, v.shape[-1], dtype=torch.float64, device="cuda") if state is None else state.double()
+    for t in range(N):
+        S = torch.baddbmm((a * S).flatten(0, 1), k[:, :, t].double().flatten(0, 1)[..., None],
+                          v[:, :, t].double().flatten(0, 1)[:, None]).view_as(S)
+    return S
+
+
+def off(got, want):
+    """Relative 2-norm of the difference, for each head."""
+    d = (got.double() - want).transpose(0, 1).flatten(1).norm(dim=1)
+    return (d / want.transpose(0, 1).flatten(1).norm(dim=1)).tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linattn_single_tokens_do_not_drift(dtype):
+    """Thousands of single tokens with slow decays.  A step rounds the new state, off by at most 2^-24 of it and to
+    either side, and the state grows with the root of the steps: T of them add up to at most sqrt(T) 2^-24 in the 2-norm.
+    (One-signed errors of a decay rounded to fp32, 2^-25 a step, would reach T / 2 times that: 6e-5.)
+    "To either side" needs low bits to round: a product of two bf16 numbers has 16, so that with |s| up to 2^8 times the
+    products the sum of a step lies on fp32's grid but for the decay's part, |log a| |s|.  Where that is below half the
+    grid's spacing (at most 2^-24 |s|), rounding to nearest drops it in every step, whatever the decay's precision: what
+    a token adds misses at most T |log a|."""
+    g, dt = gen(60), TORCH[dtype]
+    B, H, T, d = 2, len(SLOW), 4096, 64
+    q, k, v = (normal(g, B, H, T, d, dtype=dt) for _ in range(3))
+    plan = mixers().LinearAttentionPlan(B, H, 1, d, d, SLOW, dtype=dtype)
+    state = torch.zeros(B, H, d, d, device="cuda")
+    for t in range(T):
+        plan.step(q[:, :, t], k[:, :, t], v[:, :, t], state)
+    rel = off(state, recurrence(k, v, SLOW))
+    bound = [T ** 0.5 * 2.0 ** -24 + (T * -x if dtype == "bf16" and -x < 2.0 ** -24 else 0.0) for x in SLOW]
+    assert all(r <= b for r, b in zip(rel, bound)), (rel, bound)
+
+
+def test_linattn_single_tokens_keep_infinite_states():
+    g = gen(61)
+    q, k, v = (normal(g, 1, 3, 64) for _ in range(3))
+    state = normal(g, 1, 3, 64, 64)
+    state[0, :, 3, 5], state[0, :, 4, 6], state[0, :, 5, 7] = math.inf, -math.inf, math.nan
+    plan = mixers().LinearAttentionPlan(1, 3, 1, 64, 64, [-0.1, -1e-5, 0.0], dtype="f32")
+    plan.step(q, k, v, state)
+    assert (state[0, :, 3, 5] == math.inf).all() and (state[0, :, 4, 6] == -math.inf).all()
+    assert torch.isnan(state).sum() == 3 and torch.isnan(state[0, :, 5, 7]).all()
