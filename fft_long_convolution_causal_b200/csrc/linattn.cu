@@ -279,13 +279,13 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
         if (STATES || ch + 1 < nch || (!at.split && p.s_out)) {
             // S <- a^L S + s_u sum_j a^(..) y_j^T z_j
             constexpr int kSteps = FULL ? 2 : 1;  // into one u; with the conditions on tiles beside it, two spill
-            const float fl = pw[L];
+            const float2 fl = a.decay[h * kLaPowers + L];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st[m][q][e] *= fl;
+                    for (int e = 0; e < 4; ++e) st[m][q][e] = decayed(fl, st[m][q][e], 0.f);
 #pragma unroll 1
             for (int k = 0; k < L; k += 8 * kSteps) {  // rows behind the length are zeros
                 float u[MT][NT][4];
@@ -338,14 +338,16 @@ constexpr int kCarryThreads = 128;
 __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant__ Args a, const double* __restrict__ lg) {
     const LaPass& p = a.p[blockIdx.z];
     let_next_start();
-    __shared__ float decay[kLaMaxSegments];  // over a segment; below zero: an empty one
+    __shared__ float2 decay[kLaMaxSegments];  // over a segment, in two parts; below zero: an empty one
     const int bh = a.whole + blockIdx.y, b = bh / a.H, h = bh % a.H, n = p.dx * p.dz;
     const int64_t len = live_tokens(a, b);
     for (int k = threadIdx.x; k < a.nseg; k += kCarryThreads) {
         const int sg = p.reverse ? a.nseg - 1 - k : k;
         const int64_t live = min(a.seg, len - sg * a.seg);
         // an empty segment passes the state on (also where the decay is zero)
-        decay[k] = live > 0 ? (float)exp(lg[h] * (double)live) : -1.f;
+        const double d = live > 0 ? exp(lg[h] * (double)live) : -1.0;
+        const float hi = __double2float_rd(d), lo = (float)(d - hi);
+        decay[k] = make_float2(hi, hi >= 0x1p-100f ? fmaxf(lo, 0x1p-149f) : lo);  // as the plan's table
     }
     __syncthreads();
     after_previous();
@@ -372,11 +374,11 @@ __global__ void __launch_bounds__(kCarryThreads) la_carry(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (k0 + i < a.nseg) {
-                const float f = decay[k0 + i];
+                const float2 f = decay[k0 + i];
                 store4(w + (k0 + i) * step, s);
-                if (f >= 0.f) {
-                    s.x = fmaf(f, s.x, own[i].x), s.y = fmaf(f, s.y, own[i].y);
-                    s.z = fmaf(f, s.z, own[i].z), s.w = fmaf(f, s.w, own[i].w);
+                if (f.x >= 0.f) {
+                    s.x = decayed(f, s.x, own[i].x), s.y = decayed(f, s.y, own[i].y);
+                    s.z = decayed(f, s.z, own[i].z), s.w = decayed(f, s.w, own[i].w);
                 }
             }
     }
@@ -576,6 +578,7 @@ cudaError_t launch_la(const fftconv_linattn_s& p, const LaCall& c, cudaStream_t 
     a.N = c.N;
     a.lengths = c.lengths;
     a.pw = p.d_pow;
+    a.decay = p.d_decay;
     a.work = c.work;
     a.state_floats = (size_t)p.dk * p.dv;
     a.pass_floats = (size_t)(bh - a.whole) * a.nseg * a.state_floats;

@@ -17,6 +17,7 @@ struct Args {
     int64_t N, seg;             // tokens, tokens a segment
     const int32_t* lengths;
     const float* pw;            // [H][kLaPowers]
+    const float2* decay;        // the same in two parts
     float* work;                // [pass][split row][nseg][dk * dv]: segment states
     size_t pass_floats, state_floats;
 };

@@ -36,8 +36,8 @@
 //
 // Rounded to bf16 once each: P' and the copy of S that inter reads (each off by
 // 2^-9 of its values, like the operands beside them), and the outputs.  la_main's
-// own S stays in the accumulator: what its truncation costs (7e-6 over 256 chunks)
-// is far below that.
+// own S stays in the accumulator: what its truncation (7e-6 over 256 chunks) and a
+// decay rounded to fp32 (2^-25 a chunk) cost is far below that.
 //
 // Bound by shared memory (operands of the products, tiles in and out, P' and the
 // split: 4500 cycles of it a chunk of 128 x 128, which takes 5900) and, in long
@@ -791,7 +791,7 @@ la_states(const __grid_constant__ Args g) {
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
-            const float f = m.pw[sp.tokens(n)];
+            const float2 f = a.decay[(size_t)h * kLaPowers + sp.tokens(n)];
             if (!(ok = wait.all(m.ufull[n & 1], (uint32_t)(n / 2) & 1u))) break;
             um::fence_after();
             const uint32_t tu = tl + K::kU + (uint32_t)(n & 1) * DZ;
@@ -804,7 +804,7 @@ la_states(const __grid_constant__ Args g) {
                     um::wait_ld<16>(u);
                     um::wait_ld<16>(s);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = as_u(fmaf(f, as_f(s[i]), as_f(u[i])));
+                    for (int i = 0; i < 16; ++i) u[i] = as_u(la::decayed(f, as_f(s[i]), as_f(u[i])));
                     um::st32x32_x16(ts + n0, u);
                 }
                 um::wait_st();

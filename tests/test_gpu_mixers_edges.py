@@ -125,3 +125,76 @@ def test_linattn_single_tokens_keep_infinite_states():
     plan.step(q, k, v, state)
     assert (state[0, :, 3, 5] == math.inf).all() and (state[0, :, 4, 6] == -math.inf).all()
     assert torch.isnan(state).sum() == 3 and torch.isnan(state[0, :, 5, 7]).all()
+
+
+# Relative 2-norms.  A sum's roundings to fp32 are off by at most 2^-24 of the partial sum each, to either side, and a
+# partial sum grows with the root of its terms: n of them add up to at most sqrt(n) 2^-24.  What has one sign is the
+# tensor core's truncation inside a partial sum that starts from zero: at most 16 accumulations on top of a sum of its
+# final size (states in bf16: of 24 products of a chunk the first eight are those of the small terms), 2^-24 each in the
+# mean, so 2^-20 of what a chunk adds; fp32 has at most 4 of them, 2^-22, and drops products below 2^-24.
+# One of three bf16 terms lost would cost 2.5e-6 of the states, one accumulator for all chunks 4e-6 to 7e-6.
+def state_bound(dtype, N):
+    if dtype == "bf16":
+        return math.ceil(N / 128) ** 0.5 * 2.0 ** -24 + 2.0 ** -20
+    return (math.ceil(N / 64) * (64 // 16 + 1)) ** 0.5 * 2.0 ** -24 + 2.0 ** -22
+
+
+def output_bound(N, d):  # fp32: sums over d and 64 tokens in steps of 16, and the state's
+    return state_bound("f32", N) + (d / 8 + 4) ** 0.5 * 2.0 ** -24 + 2.0 ** -22
+
+
+def last_state(k, v, log_decay, state=None):
+    """The last state by the direct sum in 64 bits: k, v [H, N, d]."""
+    N = k.shape[1]
+    left = torch.arange(N - 1, -1, -1, device="cuda").double()
+    g = torch.tensor(log_decay, dtype=torch.float64, device="cuda")[:, None]
+    S = (k.double() * torch.exp(g * left)[..., None]).transpose(1, 2) @ v.double()
+    return S if state is None else S + torch.exp(g * N)[..., None] * state.double()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [59, 1])
+def test_linattn_long_rows_do_not_drift(rows, dtype):
+    """Hundreds of chunks of rows that run whole (59 x 5 of them fill the GPU once) and in segments (5), from large
+    states, with slow decays; the fourth's power over a chunk lies halfway between two fp32 numbers (an error of 2^-25 a
+    chunk, always to one side, would reach 4e-6 in bf16, 8e-6 in fp32)."""
+    g, dt = gen(62), TORCH[dtype]
+    H, N, d = 5, 32768, 64
+    lg = [-0.0123, -3.35e-4, -1e-5, -100.5 * 2.0 ** -24 / (128 if dtype == "bf16" else 64), -2e-8]
+    q, k, v = (normal(g, 1, H, N, d, dtype=dt) for _ in range(3))
+    s0 = 64 * normal(g, 1, H, d, d)
+    plan = mixers().LinearAttentionPlan(rows, H, N, d, d, lg, dtype=dtype)
+    many = [t.expand(rows, H, N, d) for t in (q, k, v)]
+    o, s = plan.fwd(*many, state=s0.expand(rows, H, d, d).contiguous(), final_state=True)
+    want = last_state(k[0], v[0], lg, s0[0])[None]
+    assert torch.equal(s, s[:1].expand_as(s))
+    rel = off(s[:1], want)
+    assert max(rel) <= state_bound(dtype, N), (rel, state_bound(dtype, N))
+    if dtype == "f32":  # the last outputs, from the state before them
+        end = N - 200
+        before = last_state(k[0, :, :end], v[0, :, :end], lg, s0[0])
+        last, _ = base.linattn(*(t[:, :, end:] for t in (q, k, v)), lg, plan.scale, before[None])
+        rel = off(o[:1, :, end:], last)
+        assert max(rel) <= output_bound(N, d), (rel, output_bound(N, d))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,N,dk,dv,layout", [s for s in base.SIZES if s[0] * s[1] * s[3] * s[4] >= 1000])
+def test_linattn_norms(B, H, N, dk, dv, layout, dtype):
+    """States and, in fp32, outputs and gradients by their 2-norm, which sees the loss of one small term."""
+    g, dt = gen(N + dk + dv), TORCH[dtype]
+    q, k, v, do = (base.tokens(g, B, H, N, d, dt, layout) for d in (dk, dk, dv, dv))
+    s0, ds = normal(g, B, H, dk, dv), normal(g, B, H, dk, dv)
+    lg = base.decays(H, "slow")
+    plan = mixers().LinearAttentionPlan(B, H, N, dk, dv, lg, dtype=dtype)
+    o, s1 = plan.fwd(q, k, v, state=s0, final_state=True)
+    want = base.linattn(q, k, v, lg, plan.scale, s0)
+    got = plan.bwd(do, q, k, v, state=s0, dstate=ds)
+    grads = base.gradients((q, k, v, s0), do, ds, lg, plan.scale, None)
+    pairs = [("state", s1, want[1]), ("dstate", got["dstate"], grads[3])]
+    if dtype == "f32":
+        pairs += [("o", o, want[0])] + [(n, got[n], t) for n, t in zip(("dq", "dk", "dv"), grads)]
+    for name, x, y in pairs:
+        rel = float((x.double() - y).norm() / y.norm())
+        bound = state_bound(dtype, N) if "state" in name else output_bound(N, max(dk, dv))
+        assert rel <= bound, (name, rel, bound)
