@@ -2,9 +2,12 @@
 
 ``python -m fft_long_convolution_causal_b200.build`` (or build()) compiles
 every .cu file under csrc/ into one shared library next to this file.  The
-library is rebuilt when any source or header is newer than it, from the objects
-whose own source and included files have not changed.
+library is rebuilt when any source or header is newer than it or when it was
+built by other commands or another nvcc, from the objects of which neither the
+commands nor the source and included files have changed.  A file <output>.key
+beside the library and each object says what built it.
 """
+import functools
 import glob
 import os
 import subprocess
@@ -22,6 +25,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
+LINK = ["-lcudart_static", "-lrt", "-lpthread", "-ldl"]
 
 
 def _sources():
@@ -33,19 +37,46 @@ def _deps():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+@functools.lru_cache(maxsize=None)
+def _version(nvcc: str) -> str:
+    try:
+        return subprocess.run([nvcc, "--version"], capture_output=True, text=True).stdout
+    except OSError:
+        return ""
+
+
+def _key() -> str:
+    """What the objects and the library depend on beside their sources; wherever the tree is."""
+    return "\n".join([NVCC, *ARCH, *FLAGS, *LINK]).replace(ROOT, ".") + "\n" + _version(NVCC)
+
+
+def _built_alike(output: str) -> bool:
+    try:
+        with open(output + ".key") as f:
+            return f.read() == _key()
+    except OSError:
+        return False
+
+
+def _say_built(output: str):
+    with open(output + ".key", "w") as f:
+        f.write(_key())
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not _built_alike(LIB):
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
 def _fresh(obj) -> bool:
-    """The object is newer than every file its compilation read."""
+    """The object was compiled alike and is newer than every file its compilation read."""
     try:
         t = os.path.getmtime(obj)
-        deps = open(obj + ".d").read().split(":", 1)[1].replace("\\\n", " ").split()
-        return bool(deps) and all(os.path.getmtime(f) <= t for f in deps)
+        with open(obj + ".d") as f:
+            deps = f.read().split(":", 1)[1].replace("\\\n", " ").split()
+        return _built_alike(obj) and bool(deps) and all(os.path.getmtime(f) <= t for f in deps)
     except (OSError, IndexError):
         return False
 
@@ -54,12 +85,15 @@ def _compile(src, verbose, force=True):
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
     if not force and not verbose and _fresh(obj):
         return obj, ""
+    if os.path.exists(obj + ".key"):  # a compilation that is cut short leaves no key
+        os.remove(obj + ".key")
     cmd = [NVCC, *ARCH, *FLAGS, "-MD", "-MF", obj + ".d", "-c", src, "-o", obj]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+    _say_built(obj)
     return obj, r.stderr
 
 
@@ -77,11 +111,12 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
             sys.stderr.write(log)
     objs = [o for o, _ in results]
     tmp = LIB + ".tmp"
-    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-lpthread", "-ldl"]
+    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, *LINK]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _say_built(LIB)
     return LIB
 
 
