@@ -47,6 +47,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <numeric>
+
 #include "linattn.cuh"
 #include "umma.cuh"
 
@@ -118,9 +120,10 @@ __device__ __forceinline__ constexpr uint64_t mnstep(int k) { return (uint64_t)(
 struct Source {
     CUtensorMap map;
     int at_token, at_head, at_row;  // dimension 1 .. 3 of each, 0: not a dimension (stride zero or one element)
-    int by_hand;                    // no map: copied with plain loads
+    int head_step, row_step;        // coordinates from one to the next
+    int by_hand;                    // no map: copied with plain loads and stores
     __device__ __forceinline__ int at(int dim, int t, int h, int b) const {
-        return at_token == dim ? t : at_head == dim ? h : at_row == dim ? b : 0;
+        return at_token == dim ? t : at_head == dim ? h * head_step : at_row == dim ? b * row_step : 0;
     }
 };
 constexpr int kMaxSources = 4 + kLaMaxPasses;
@@ -352,8 +355,17 @@ la_main(const __grid_constant__ Args g) {
     // the outputs of chunk n, staged in z's tile, go out as a bulk copy
     auto store = [&](int n) {
         if (!wait.all(m.staged[n & 1], (uint32_t)(n >> 1) & 1u)) return false;
-        if (lane == 0) {
-            const Source& so = g.src[g.out[at.pass]];
+        const Source& so = g.src[g.out[at.pass]];
+        if (so.by_hand) {
+            const int64_t t0 = sp.start(n);
+            __nv_bfloat16* out = (__nv_bfloat16*)p.out + b * p.so.batch + h * p.so.head + (sp.first + t0) * p.so.token;
+            const int rows = (int)min((int64_t)kC, sp.rows - t0), cols = p.dz / 8;
+#pragma unroll 1
+            for (int e = lane; e < rows * cols; e += 32) {
+                const int t = e / cols, c = e - t * cols;
+                *reinterpret_cast<uint4*>(out + t * p.so.token + 8 * c) = lds128(tile(n, 2) + tile_off(t, c));
+            }
+        } else if (lane == 0) {
             const int tk = (int)(sp.first + sp.start(n));
             const int c1 = so.at(1, tk, h, b), c2 = so.at(2, tk, h, b), c3 = so.at(3, tk, h, b);
 #pragma unroll 1
@@ -852,13 +864,20 @@ EncodeFn encoder() {
     return fn;
 }
 
-// The map of a tensor [B][H][N][d]: dimensions in the order of their strides, those that do not move left out.
+// The map of a tensor [B][H][N][d]: dimensions in the order of their strides, those that do not move left out.  A map's
+// strides have to be multiples of one another.  Where a head's or a row's is not what the next one needs (heads of 64 in
+// tokens of 3 x 224, say), its dimension goes in steps of their greatest common divisor and it takes several of them; a
+// box has to go by tokens, so where the tokens' stride would need that (or all tokens are one) the tensor is copied by
+// hand (8 x 11 x 4096 of 64 with such strides 165 us, 79 by maps; all tensors at 64 and 96 in one projection 408 by hand,
+// 101 by maps in steps, 99 dense).
 void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int H, int64_t N, int d) {
     struct Dim {
         int64_t extent, stride;
         int* at;
-    } dim[3] = {{N, st.token, &s->at_token}, {H, st.head, &s->at_head}, {B, st.batch, &s->at_row}};
+        int* step;
+    } dim[3] = {{N, st.token, &s->at_token, nullptr}, {H, st.head, &s->at_head, &s->head_step}, {B, st.batch, &s->at_row, &s->row_step}};
     s->at_token = s->at_head = s->at_row = 0;
+    s->head_step = s->row_step = 1;
     s->by_hand = 1;
     const EncodeFn enc = encoder();
     if (!enc || (N > 1 && st.token == 0) || N > 0x7fffffff) return;
@@ -872,6 +891,15 @@ void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int 
             use[j] = use[j - 1];
             use[j - 1] = t;
         }
+    if (n && use[0].stride < 0) return;
+    for (int i = n - 2; i >= 0; --i) {
+        const int64_t unit = std::gcd(use[i].stride, use[i + 1].stride), steps = use[i].stride / unit;
+        if (steps == 1) continue;
+        if (!use[i].step || (use[i].extent - 1) > 0x7ffffffe / steps) return;
+        *use[i].step = (int)steps;
+        use[i].extent = (use[i].extent - 1) * steps + 1;
+        use[i].stride = unit;
+    }
     cuuint64_t dims[4] = {(cuuint64_t)d, 1, 1, 1}, strides[3];
     cuuint32_t box[4] = {64, 1, 1, 1}, one[4] = {1, 1, 1, 1};
     cuuint64_t last = (cuuint64_t)d * 2;
@@ -950,7 +978,6 @@ cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool end
         g.y[i] = source(q.y, q.sy, q.dx);
         g.z[i] = source(q.z, q.sz, q.dz);
         g.out[i] = source(q.out, q.so, q.dz);
-        if (g.src[g.out[i]].by_hand) return cudaErrorInvalidValue;
     }
     const int bh = B * a.H;
     if (dx <= 64)

@@ -466,8 +466,9 @@ FFTCONV_API fftconv_status fftconv_device_status(fftconv_plan_t plan, void* stre
  * the stream without synchronising) with these additions:
  *   - B and N of a plan are the largest of a call; each call gives its own.
  *   - Token tensors are strided views [B][H][N][d] whose last dimension is
- *     contiguous; strides are in elements and multiples of 16 bytes.  An input
- *     may have a stride of zero (a head shared by all); an output may not.
+ *     contiguous; strides are in elements and multiples of 16 bytes (rotary:
+ *     of an element).  An input may have a stride of zero (a head shared by
+ *     all) or overlap itself; an output may not.
  *   - Calls of one plan may run on several streams at once, each with its own
  *     workspace (and distinct outputs).  Every call but plan creation,
  *     destruction and *_device_status may be captured into a CUDA graph under

@@ -198,3 +198,50 @@ def test_linattn_norms(B, H, N, dk, dv, layout, dtype):
         rel = float((x.double() - y).norm() / y.norm())
         bound = state_bound(dtype, N) if "state" in name else output_bound(N, max(dk, dv))
         assert rel <= bound, (name, rel, bound)
+
+
+def odd_views(g, kind, B, H, N, dims, dt):
+    """[B, H, N, d] views for each d whose strides are no multiples of one another (or whose rows overlap), and the
+    buffers they lie in."""
+    if kind == "fused":  # one projection of all of them
+        buf = normal(g, B, N, H * sum(dims), dtype=dt)
+        views, at = [], 0
+        for d in dims:
+            views.append(buf[..., at:at + H * d].view(B, N, H, d).transpose(1, 2))
+            at += H * d
+        return views, [buf] * len(dims)
+    if kind == "padded heads":  # a head's tokens side by side, eight elements between heads
+        bufs = [normal(g, B * (H * (N * d + 8)) + 8, dtype=dt) for d in dims]
+        return [b.as_strided((B, H, N, d), (H * (N * d + 8), N * d + 8, d, 1)) for b, d in zip(bufs, dims)], bufs
+    assert kind == "windows"  # token t starts eight elements behind token t - 1
+    bufs = [normal(g, B, H, 8 * N + d, dtype=dt) for d in dims]
+    return [b.as_strided((B, H, N, d), (H * (8 * N + d), 8 * N + d, 8, 1)) for b, d in zip(bufs, dims)], bufs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["fused", "padded heads", "windows"])
+@pytest.mark.parametrize("B,H,N,dk,dv", [(2, 3, 1, 64, 96), (2, 3, 130, 64, 96), (2, 3, 700, 40, 104), (1, 5, 1000, 128, 72),
+                                         (60, 5, 300, 64, 40)])
+def test_linattn_strides_that_are_no_multiples(B, H, N, dk, dv, kind, dtype):
+    """The same bits as dense copies give, and outputs that touch only their elements."""
+    g, dt = gen(N + dv), TORCH[dtype]
+    (q, k, v, do), _ = odd_views(g, kind, B, H, N, (dk, dk, dv, dv), dt)
+    dense = [t.clone(memory_format=torch.contiguous_format) for t in (q, k, v, do)]
+    lg = base.decays(H)
+    plan = mixers().LinearAttentionPlan(B, H, N, dk, dv, lg, dtype=dtype)
+    lengths = torch.randint(0, N + 1, (B,), generator=g, device="cuda").int()
+    for n in (None, lengths):
+        o, s = plan.fwd(*dense[:3], lengths=n, final_state=True)
+        got, end = plan.fwd(q, k, v, lengths=n, final_state=True)
+        assert torch.equal(got, o) and torch.equal(end, s)
+        if kind != "windows":
+            (_, _, out, _), bufs = odd_views(g, kind, B, H, N, (dk, dk, dv, dv), dt)
+            bufs[2].fill_(7.0)
+            plan.fwd(*dense[:3], lengths=n, o=out)
+            assert torch.equal(out, o)
+            out.fill_(7.0)
+            assert (bufs[2] == 7.0).all()
+        want = plan.bwd(dense[3], *dense[:3], lengths=n)
+        got = plan.bwd(do, q, k, v, lengths=n)
+        assert all(torch.equal(got[x], want[x]) for x in ("dq", "dk", "dv"))
+    assert plan.device_status() == 0
