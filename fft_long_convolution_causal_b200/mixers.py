@@ -371,10 +371,6 @@ class RetentionPlan:
         self.norm = LayerNormPlan(B * H * N, dv, dtype=dtype, groups=H, eps=eps)
         self.H = H
 
-    def _token_major(self, t):
-        """[B, H, N, d] as dense rows (b, n, h), the order the norm's weights repeat in."""
-        return t.transpose(1, 2).contiguous()
-
     def fwd(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor,
             positions: torch.Tensor, state: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
             final_state: bool = False, save: bool = False, stream=None):
@@ -383,9 +379,13 @@ class RetentionPlan:
         bwd needs.  (The norm of a row behind a length is its bias.)"""
         with self.attention._on(stream):
             qr, kr = self.rotary.apply(q, k, positions=positions, stream=stream)
-            got = self.attention.fwd(qr, kr, v, state=state, lengths=lengths, final_state=final_state, stream=stream)
-            o, end = got if final_state else (got, None)
-            rows = self._token_major(o)
+            # token by token: the order the norm's weights repeat in
+            B, _, N, _ = qr.shape
+            rows = torch.empty((B, N, self.H, self.attention.dv), dtype=self.attention.torch_dtype,
+                               device=self.attention.device)
+            got = self.attention.fwd(qr, kr, v, state=state, lengths=lengths, final_state=final_state,
+                                     o=rows.transpose(1, 2), stream=stream)
+            end = got[1] if final_state else None
             y, mean, rstd = self.norm.fwd(rows, weight, bias, statistics=True, stream=stream)
         out = [y] + ([end] if final_state else []) + ([(qr, kr, v, state, lengths, positions, rows, mean, rstd)]
                                                       if save else [])

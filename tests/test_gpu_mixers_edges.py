@@ -245,3 +245,34 @@ def test_linattn_strides_that_are_no_multiples(B, H, N, dk, dv, kind, dtype):
         got = plan.bwd(do, q, k, v, lengths=n)
         assert all(torch.equal(got[x], want[x]) for x in ("dq", "dk", "dv"))
     assert plan.device_status() == 0
+
+
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+def test_retention_runs_no_other_kernels(layout):
+    """Every step is one of the library's: torch allocates and makes views, whatever order the tokens are stored in."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Record(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.names = set()
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.names.add(func.overloadpacket.__name__)
+            return func(*args, **(kwargs or {}))
+
+    g = gen(70)
+    B, H, N, dk, dv = 2, 3, 150, 64, 96
+    q, k, v = (base.tokens(g, B, H, N, d, torch.bfloat16, layout) for d in (dk, dk, dv))
+    w, b, at = 1 + 0.2 * normal(g, H, dv), 0.2 * normal(g, H, dv), torch.arange(N, device="cuda")
+    plan = mixers().RetentionPlan(B, H, N, dk, dv)
+    state, dy = normal(g, B, H, dk, dv), normal(g, B, N, H, dv, dtype=torch.bfloat16)
+    with Record() as seen:
+        y, end, saved = plan.fwd(q, k, v, w, b, at, state=state, final_state=True, save=True)
+        plan.bwd(dy, saved, w)
+        plan.step(q[:, :, 0], k[:, :, 0], v[:, :, 0], w, b, at[:B], end)
+    assert seen.names <= {"empty", "empty_like", "empty_strided", "view", "transpose", "unsqueeze", "squeeze", "select",
+                          "slice", "detach", "alias", "as_strided"}, seen.names
+    qr, kr = plan.rotary.apply(q, k, positions=at)
+    o = plan.attention.fwd(qr, kr, v, state=state)
+    assert torch.equal(y, plan.norm.fwd(o.transpose(1, 2).contiguous(), w, b))
