@@ -475,10 +475,12 @@ cudaError_t pick(int C, F f) {
     if (items <= 32) return f.template operator()<T, V, 16, 2, true>();
     if (items <= 48) return f.template operator()<T, V, 16, 3, true>();
     if (items <= 64) return f.template operator()<T, V, 32, 2, true>();
-    if (F::kThree && items <= 96) return f.template operator()<T, V, 32, 3, true>();
+    if constexpr (F::kThree)
+        if (items <= 96) return f.template operator()<T, V, 32, 3, true>();
     if (items <= 128) return f.template operator()<T, V, 128, 1, true>();
     if (items <= 256) return f.template operator()<T, V, 128, 2, true>();
-    if (F::kThree && items <= 384) return f.template operator()<T, V, 128, 3, true>();
+    if constexpr (F::kThree)
+        if (items <= 384) return f.template operator()<T, V, 128, 3, true>();
     if (items <= 512) return f.template operator()<T, V, 512, 1, true>();
     if (items <= 1024) return f.template operator()<T, V, 512, 2, true>();
     if (items <= 1536) return f.template operator()<T, V, 512, 3, true>();
