@@ -289,8 +289,9 @@ fftconv_status fftconv_norm_plan_create(fftconv_norm** out, int64_t rows, int C,
                                         const double* eps) {
     if (!out) return FFTCONV_ERR_INVALID_ARG;
     *out = nullptr;
+    // in fp32 an eps that is not zero stays so (a row of one value would give 0 x infinity), and finite
     if (rows < 1 || C < 1 || groups < 1 || rows % groups || !valid_dtype(dtype) || !eps || !(*eps >= 0.0) ||
-        !isfinite(*eps))
+        !isfinite((float)*eps) || (*eps > 0.0 && (float)*eps == 0.f))
         return FFTCONV_ERR_INVALID_ARG;
     if (C > FFTCONV_NORM_MAX_C || groups > 65535 || rows > 2147483647) return FFTCONV_ERR_UNSUPPORTED;
     fftconv_norm_s* p = new (std::nothrow) fftconv_norm_s();

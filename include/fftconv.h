@@ -634,8 +634,9 @@ FFTCONV_API fftconv_status fftconv_rotary_apply(const fftconv_rotary* plan, cons
  *     y = (x - mean) rstd w + b,   rstd = 1 / sqrt(var + eps)
  * x, y: [rows][C] dense, of the plan's dtype; w, b: [groups][C] fp32, row r
  * uses row r mod groups (1: one weight; the number of heads: the norm behind
- * each head of [..][heads][C]).  Statistics in fp32.  `rows` of a call is at
- * most the plan's and a multiple of groups.
+ * each head of [..][heads][C]).  Statistics in fp32: eps is zero or an fp32
+ * number after rounding, and with zero a row of one value gives NaN, as 0 / 0.
+ * `rows` of a call is at most the plan's and a multiple of groups.
  */
 #define FFTCONV_NORM_MAX_C 16384
 FFTCONV_API fftconv_status fftconv_norm_plan_create(fftconv_norm** plan, int64_t rows, int C, int groups,
