@@ -30,7 +30,10 @@ __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<f
 
 // ---- fp32 on the tensor cores: every operand as a sum of two tf32 values (the
 // second exact to 2^-23 of the first's), three products, the largest last.  The
-// product of the two small parts, below 2^-24, is left out.
+// product of the two small parts, below 2^-22, is left out.  Below 2^-114 the second
+// part is a subnormal number and loses bits; within 2^-12 of the largest number the
+// first is an infinity (kept finite by one instruction more a value, 24 x 4096 x 64
+// took 121 us instead of 115).
 struct Two {
     uint32_t hi, lo;
 };

@@ -490,15 +490,19 @@ typedef struct {
  * q, k: [B][H][N][dk], v, o: [B][H][N][dv] of the plan's dtype; the state S
  * [dk][dv] in fp32, S_{-1} = state_in or zero.  dk and dv are multiples of 8
  * in [8, FFTCONV_LINATTN_MAX_DIM].  log_decay is a host array of H values
- * <= 0 (minus infinity: only the token itself), constants of the plan.  bf16:
- * products accumulate in fp32; the scores and the copy of the state that q
- * reads are rounded to bf16 once, the state itself is not (the keys added to it
- * are split into two or three bf16 terms).  fp32: every operand is split into
- * two tf32 terms, results are those of fp32 arithmetic to a few units in the
- * last place of the sums.  An infinity gives NaN there.  Tokens are taken in
- * chunks (of 128 in bf16, 64 in fp32, from the first): a NaN or an infinity in v
- * (backward: in q, k or d_o) reaches every output of its chunk, the earlier
- * tokens' too; what lies behind a row's length is not read.
+ * <= 0 (minus infinity: only the token itself), constants of the plan.
+ *   bf16: products accumulate in fp32; the scores and the copy of the state that
+ * q reads are rounded to bf16 once each, the state itself is not (the keys added
+ * to it are split into two bf16 terms for the outputs, three for final states).
+ * With random operands outputs are off by 2.4e-3 in the 2-norm, of which their own
+ * rounding is 1.7e-3; final states by up to 1e-6, for keys from 2^-110 on.
+ *   fp32: every operand is split into two tf32 terms; results are those of fp32
+ * arithmetic to a few units in the last place of the sums, for values from 2^-114
+ * (below, they keep fewer bits: 1e-5 of a result at 2^-120) to 3.4019e38; larger
+ * ones and infinities give NaN.
+ *   Tokens are taken in chunks (of 128 in bf16, 64 in fp32, from the first): a NaN
+ * or an infinity in v (backward: in q, k or d_o) reaches every output of its chunk,
+ * the earlier tokens' too; what lies behind a row's length is not read.
  * FFTCONV_ERR_UNSUPPORTED for other dims or B H > 65535.
  */
 #define FFTCONV_LINATTN_MAX_DIM 128
@@ -590,7 +594,8 @@ FFTCONV_API fftconv_status fftconv_linattn_device_status(fftconv_linattn* plan, 
  *                          take f_i / factor, a linear ramp over i between
  *                          (its ends rounded outwards to whole pairs);
  *                          m = 0.1 ln(factor) + 1.
- * m = 1 otherwise.  Angles are exact modulo a turn for any 64-bit position.
+ * m = 1 otherwise.  Angles are reduced modulo a turn without loss; what is left is
+ * the rounding of f_i to 2^-65 turn, times the position (2^-34 turn at 2^31).
  */
 typedef enum {
     FFTCONV_ROTARY_NONE = 0,

@@ -131,7 +131,7 @@ def test_linattn_single_tokens_keep_infinite_states():
 # partial sum grows with the root of its terms: n of them add up to at most sqrt(n) 2^-24.  What has one sign is the
 # tensor core's truncation inside a partial sum that starts from zero: at most 16 accumulations on top of a sum of its
 # final size (states in bf16: of 24 products of a chunk the first eight are those of the small terms), 2^-24 each in the
-# mean, so 2^-20 of what a chunk adds; fp32 has at most 4 of them, 2^-22, and drops products below 2^-24.
+# mean, so 2^-20 of what a chunk adds; fp32 has at most 4 of them, 2^-22, and drops products of two small parts (up to 2^-22, of either sign, 4e-8 in the mean).
 # One of three bf16 terms lost would cost 2.5e-6 of the states, one accumulator for all chunks 4e-6 to 7e-6.
 def state_bound(dtype, N):
     if dtype == "bf16":
@@ -276,3 +276,28 @@ def test_retention_runs_no_other_kernels(layout):
     qr, kr = plan.rotary.apply(q, k, positions=at)
     o = plan.attention.fwd(qr, kr, v, state=state)
     assert torch.equal(y, plan.norm.fwd(o.transpose(1, 2).contiguous(), w, b))
+
+
+def test_linattn_range_of_values():
+    """fp32 values from 2^-114 (a second tf32 part is whole down to there) to 3.4019e38 (the first is finite up to there);
+    states in bf16 for keys from 2^-110 on (the third of their terms)."""
+    g = gen(71)
+    B, H, N, d = 1, 2, 200, 64
+    lg = [-0.01, -0.1]
+    q, k, v = (normal(g, B, H, N, d) for _ in range(3))
+    plan = mixers().LinearAttentionPlan(B, H, N, d, d, lg, dtype="f32")
+    for small in ((q * 2.0 ** -114, k, v), (q, k * 2.0 ** -114, v), (q, k, v * 2.0 ** -114)):
+        o, s = plan.fwd(*small, final_state=True)
+        want = base.linattn(*small, lg, plan.scale)
+        assert max(off(o, want[0])) <= output_bound(N, d) and max(off(s, want[1])) <= state_bound("f32", N)
+    w = v.clone()
+    w[:, :, 50, 3], w[:, :, 60, 4] = 3.4019e38, -3.4019e38
+    low = (q * 2.0 ** -6, k * 2.0 ** -6, w)
+    o, s = plan.fwd(*low, final_state=True)
+    want = base.linattn(*low, lg, plan.scale)
+    assert torch.isfinite(o).all() and max(off(o, want[0])) <= output_bound(N, d)
+    half = mixers().LinearAttentionPlan(B, H, N, d, d, lg)
+    keys, values = (k * 2.0 ** -110).bfloat16(), v.bfloat16()
+    _, s = half.fwd(q.bfloat16(), keys, values, final_state=True)
+    _, want = base.linattn(q.bfloat16(), keys, values, lg, half.scale)
+    assert max(off(s, want)) <= state_bound("bf16", N)
