@@ -76,6 +76,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int sr
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;\n" ::: "memory");
 }
+// (x, y) times a plus (u, v), two a time
+__device__ __forceinline__ void fma2(float a, uint32_t x, uint32_t y, uint32_t& u, uint32_t& v) {
+    asm("{\n.reg .b64 p, q, r;\nmov.b64 p, {%2, %3};\nmov.b64 q, {%4, %4};\nmov.b64 r, {%0, %1};\nfma.rn.f32x2 r, p, q, r;\n"
+        "mov.b64 {%0, %1}, r;\n}\n"
+        : "+r"(u), "+r"(v)
+        : "r"(x), "r"(y), "f"(a));
+}
 // (x, y) times (a, b), two products an instruction
 __device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
     asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}\n"
@@ -121,9 +128,9 @@ struct Source {
     CUtensorMap map;
     int at_token, at_head, at_row;  // dimension 1 .. 3 of each, 0: not a dimension (stride zero or one element)
     int head_step, row_step;        // coordinates from one to the next
-    int by_hand;                    // no map: copied with plain loads and stores
+    int by_hand;                    // no map: copied with plain loads
     __device__ __forceinline__ int at(int dim, int t, int h, int b) const {
-        return at_token == dim ? t : at_head == dim ? h * head_step : at_row == dim ? b * row_step : 0;
+        return (at_token == dim ? t : 0) + (at_head == dim ? h * head_step : 0) + (at_row == dim ? b * row_step : 0);
     }
 };
 constexpr int kMaxSources = 4 + kLaMaxPasses;
@@ -355,17 +362,8 @@ la_main(const __grid_constant__ Args g) {
     // the outputs of chunk n, staged in z's tile, go out as a bulk copy
     auto store = [&](int n) {
         if (!wait.all(m.staged[n & 1], (uint32_t)(n >> 1) & 1u)) return false;
-        const Source& so = g.src[g.out[at.pass]];
-        if (so.by_hand) {
-            const int64_t t0 = sp.start(n);
-            __nv_bfloat16* out = (__nv_bfloat16*)p.out + b * p.so.batch + h * p.so.head + (sp.first + t0) * p.so.token;
-            const int rows = (int)min((int64_t)kC, sp.rows - t0), cols = p.dz / 8;
-#pragma unroll 1
-            for (int e = lane; e < rows * cols; e += 32) {
-                const int t = e / cols, c = e - t * cols;
-                *reinterpret_cast<uint4*>(out + t * p.so.token + 8 * c) = lds128(tile(n, 2) + tile_off(t, c));
-            }
-        } else if (lane == 0) {
+        if (lane == 0) {
+            const Source& so = g.src[g.out[at.pass]];
             const int tk = (int)(sp.first + sp.start(n));
             const int c1 = so.at(1, tk, h, b), c2 = so.at(2, tk, h, b), c3 = so.at(3, tk, h, b);
 #pragma unroll 1
@@ -816,7 +814,10 @@ la_states(const __grid_constant__ Args g) {
                     um::wait_ld<16>(u);
                     um::wait_ld<16>(s);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = as_u(la::decayed(f, as_f(s[i]), as_f(u[i])));
+                    for (int i = 0; i < 16; i += 2) {  // as la::decayed
+                        fma2(f.y, s[i], s[i + 1], u[i], u[i + 1]);
+                        fma2(f.x, s[i], s[i + 1], u[i], u[i + 1]);
+                    }
                     um::st32x32_x16(ts + n0, u);
                 }
                 um::wait_st();
@@ -865,17 +866,15 @@ EncodeFn encoder() {
 }
 
 // The map of a tensor [B][H][N][d]: dimensions in the order of their strides, those that do not move left out.  A map's
-// strides have to be multiples of one another.  Where a head's or a row's is not what the next one needs (heads of 64 in
-// tokens of 3 x 224, say), its dimension goes in steps of their greatest common divisor and it takes several of them; a
-// box has to go by tokens, so where the tokens' stride would need that (or all tokens are one) the tensor is copied by
-// hand (8 x 11 x 4096 of 64 with such strides 165 us, 79 by maps; all tensors at 64 and 96 in one projection 408 by hand,
-// 101 by maps in steps, 99 dense).
+// strides have to be multiples of one another; where a view's are not (heads of 64 in tokens of 3 x 224, say), heads and
+// rows become one dimension in steps of the greatest common divisor of all strides, in front of the tokens.  (8 x 11 x
+// 4096 of 64 and 96 in one projection: 92 us, dense 90; copied by hand 408.)  Where all tokens are one, or coordinates
+// would pass 31 bits, there is no map.
 void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int H, int64_t N, int d) {
     struct Dim {
         int64_t extent, stride;
         int* at;
-        int* step;
-    } dim[3] = {{N, st.token, &s->at_token, nullptr}, {H, st.head, &s->at_head, &s->head_step}, {B, st.batch, &s->at_row, &s->row_step}};
+    } dim[3] = {{N, st.token, &s->at_token}, {H, st.head, &s->at_head}, {B, st.batch, &s->at_row}};
     s->at_token = s->at_head = s->at_row = 0;
     s->head_step = s->row_step = 1;
     s->by_hand = 1;
@@ -884,21 +883,32 @@ void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int 
     int n = 0;
     Dim use[3];
     for (const Dim& x : dim)
-        if (x.extent > 1 && x.stride != 0) use[n++] = x;
+        if (x.extent > 1 && x.stride != 0) {
+            if (x.stride < 0) return;
+            use[n++] = x;
+        }
     for (int i = 1; i < n; ++i)
         for (int j = i; j > 0 && use[j].stride < use[j - 1].stride; --j) {
             const Dim t = use[j];
             use[j] = use[j - 1];
             use[j - 1] = t;
         }
-    if (n && use[0].stride < 0) return;
-    for (int i = n - 2; i >= 0; --i) {
-        const int64_t unit = std::gcd(use[i].stride, use[i + 1].stride), steps = use[i].stride / unit;
-        if (steps == 1) continue;
-        if (!use[i].step || (use[i].extent - 1) > 0x7ffffffe / steps) return;
-        *use[i].step = (int)steps;
-        use[i].extent = (use[i].extent - 1) * steps + 1;
-        use[i].stride = unit;
+    bool chain = true;
+    for (int i = 1; i < n; ++i) chain = chain && use[i].stride % use[i - 1].stride == 0;
+    if (!chain) {
+        int64_t unit = 0, most = 1;
+        for (int i = 0; i < n; ++i) unit = std::gcd(unit, use[i].stride);
+        for (int i = 0; i < n; ++i) {
+            if (use[i].at == &s->at_token) continue;
+            const int64_t step = use[i].stride / unit;
+            if (step > 0x7fffffff || (use[i].extent - 1) > (0x7fffffff - most) / step) return;
+            most += (use[i].extent - 1) * step;
+            *use[i].at = 1;
+            (use[i].at == &s->at_head ? s->head_step : s->row_step) = (int)step;
+        }
+        use[0] = {most, unit, nullptr};
+        n = 1;
+        if (N > 1) use[n++] = dim[0];
     }
     cuuint64_t dims[4] = {(cuuint64_t)d, 1, 1, 1}, strides[3];
     cuuint32_t box[4] = {64, 1, 1, 1}, one[4] = {1, 1, 1, 1};
@@ -907,7 +917,7 @@ void describe(Source* s, const void* ptr, const fftconv_strides& st, int B, int 
         if (i < n) {
             dims[i + 1] = (cuuint64_t)use[i].extent;
             last = (cuuint64_t)use[i].stride * 2;
-            *use[i].at = i + 1;
+            if (use[i].at) *use[i].at = i + 1;
             if (use[i].at == &s->at_token) box[i + 1] = kC;
         }
         strides[i] = last;
@@ -978,6 +988,7 @@ cudaError_t launch_tc(const Args& a, int dx, int dz, int B, int passes, bool end
         g.y[i] = source(q.y, q.sy, q.dx);
         g.z[i] = source(q.z, q.sz, q.dz);
         g.out[i] = source(q.out, q.so, q.dz);
+        if (g.src[g.out[i]].by_hand) return cudaErrorNotSupported;
     }
     const int bh = B * a.H;
     if (dx <= 64)

@@ -32,7 +32,9 @@ void current_device(int* device, int* sms) {
     }
 }
 
-fftconv_status status_of(cudaError_t e) { return e == cudaSuccess ? FFTCONV_OK : FFTCONV_ERR_CUDA; }
+fftconv_status status_of(cudaError_t e) {
+    return e == cudaSuccess ? FFTCONV_OK : e == cudaErrorNotSupported ? FFTCONV_ERR_UNSUPPORTED : FFTCONV_ERR_CUDA;
+}
 
 // device copy of a host block
 fftconv_status upload(const void* host, size_t bytes, void** out) {

@@ -3,8 +3,10 @@ per head, rotary positions, layer norm, and the retention core that runs the
 three together.
 
 Argument marshalling only, as in binding.py: every step runs in the CUDA
-library.  Token tensors are [B, H, N, d] with any strides that keep the last
-dimension contiguous (pass x.transpose(1, 2) for [B, N, H, d] storage).  Work
+library.  Token tensors are [B, H, N, d] views whose last dimension is
+contiguous (pass x.transpose(1, 2) for [B, N, H, d] storage); linear attention
+takes strides that are multiples of 16 bytes, rotary any.  An output given as an
+argument overlaps no input, and tensors rotated in place not each other.  Work
 goes to `stream` (default: torch's current stream of the plan's device), outputs
 and workspaces come from torch's allocator on that stream, so calls on several
 streams and captured graphs never share scratch memory.

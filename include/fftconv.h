@@ -503,7 +503,8 @@ typedef struct {
  *   Tokens are taken in chunks (of 128 in bf16, 64 in fp32, from the first): a NaN
  * or an infinity in v (backward: in q, k or d_o) reaches every output of its chunk,
  * the earlier tokens' too; what lies behind a row's length is not read.
- * FFTCONV_ERR_UNSUPPORTED for other dims or B H > 65535.
+ * FFTCONV_ERR_UNSUPPORTED for other dims or B H > 65535, and in bf16 for outputs
+ * with negative strides or rows and heads more than 2^31 common units apart.
  */
 #define FFTCONV_LINATTN_MAX_DIM 128
 FFTCONV_API fftconv_status fftconv_linattn_plan_create(fftconv_linattn** plan, int B, int H, int64_t N, int dk,
