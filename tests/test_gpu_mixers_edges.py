@@ -301,3 +301,31 @@ def test_linattn_range_of_values():
     _, s = half.fwd(q.bfloat16(), keys, values, final_state=True)
     _, want = base.linattn(q.bfloat16(), keys, values, lg, half.scale)
     assert max(off(s, want)) <= state_bound("bf16", N)
+
+
+def test_linattn_negative_strides():
+    """Tokens stored backwards, through the C call: read and (fp32) written so; bf16 outputs are refused before anything runs."""
+    g, m = gen(72), mixers()
+    B, H, N, d = 1, 2, 150, 64
+    for dtype in ("f32", "bf16"):
+        q, k, v = (normal(g, B, H, N, d, dtype=TORCH[dtype]) for _ in range(3))
+        plan = m.LinearAttentionPlan(B, H, N, d, d, [-0.1, -0.01], dtype=dtype)
+        want = plan.fwd(q, k, v)
+        back = q.flip(2)  # token t of q is row N - 1 - t
+        forth, reverse = (0, N * d, d), (0, N * d, -d)
+        last = (N - 1) * d * q.element_size()
+
+        def call(out, so, end):
+            a = m._FWD.pack(m._FWD.size, B, N, plan.scale, back.data_ptr() + last, k.data_ptr(), v.data_ptr(), *reverse,
+                            *forth, *forth, 0, 0, out.data_ptr() + end, *so, 0)
+            ws = plan._workspace(0)
+            return plan.lib.fftconv_linattn_fwd(plan._handle, a, ws.data_ptr(), plan._stream(None))
+
+        o = torch.full_like(v, 7.0)
+        assert call(o, forth, 0) == 0 and torch.equal(o, want)
+        o.fill_(7.0)
+        status = call(o, reverse, last)
+        if dtype == "f32":
+            assert status == 0 and torch.equal(o.flip(2), want)
+        else:
+            assert status == 2 and (o == 7.0).all()
