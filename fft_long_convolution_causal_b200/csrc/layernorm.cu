@@ -5,18 +5,21 @@
 // Row r uses weight row r mod G (G = 1: one weight for all; G = heads: the norm
 // behind each head).
 //
-// Bound by memory.  A row is read once into registers (mean first, then the sum
+// Moves each tensor once (x twice, both ways together), at two thirds of the copy
+// rate: what is left is the loads' latency (the backward pass has 12 warps an SM with
+// one row of loads ahead; its issue slots are 53% used) and the launches' ramps.  A row is read once into registers (mean first, then the sum
 // of centred squares: no cancellation) by TPR threads, each holding E pieces of
 // 16 bytes.  Where C is not a multiple of a piece (OFF), a row starts up to a piece
 // behind a 16-byte boundary: pieces lie on the boundaries all the same, the two
 // at the row's ends are read and written by elements, and a thread walks rows in
 // steps that keep its columns, with their weights in registers.  38668 x 557 bf16
-// both ways: 318 us with one element a piece, 108 us so.  The weight
+// both ways: 318 us with one element a piece, 111 us so.  The weight
 // gradient is summed over the rows a block walks in registers, then over blocks
 // by a second kernel in a fixed order: repeated calls agree bit for bit.
-// 32768 x 768 bf16: forward 22.9 us (4.4 TB/s of x and y), backward 35.3 us
-// (4.3 TB/s of dy, x and dx), the launches' ramps included; 49152 x 64 fp32
-// forward 9.4 us, 17 x 2708 both ways 31 us, which is the host's time.
+// 32768 x 768 bf16: forward 23.1 us (4.4 TB/s of x and y), backward 35.9 us
+// (4.2 TB/s of dy, x and dx), the launches' ramps included; 16384 x 768 fp32 19.0
+// (5.3 TB/s) and 41.6 us (3.6 TB/s); 49152 x 64 fp32 forward 9.0 us, 17 x 2708 both
+// ways 31 us, which is the host's time.
 #include <cuda_bf16.h>
 
 #include "linattn.cuh"

@@ -128,11 +128,14 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
 // tile of theirs from w >> 2 on (tiles behind dz are left out); the state lives
 // in registers as accumulators (m-tiles w & 3, + 4), with a copy in shared
 // memory for the outputs.  Two CTAs of 8 warps an SM at 64 x 64, one of 16 above.
-// Bound by issue: a product of 16 x 8 x 8 comes with ten instructions (its
-// operands' loads and splits, its share of the sums), issued in 53% of the slots,
-// and the tensor pipe is busy 42% of the time.  24 rows x 4096 at 64 x 64 take
-// 114 us (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 110 to 145 us
-// (as its lengths fall); fp32 multiplications without the tensor cores took 242 and 363.
+// Bound by the chain of a chunk's steps, with one or two CTAs an SM to hide it:
+// its copies are waited for, four barriers part the steps, and every product loads
+// and splits its operands anew (ten instructions a 16 x 8 x 8).  Neither the issue
+// slots (52% used) nor the tensor pipe (42%) are full; warps wait for fixed
+// latencies (1.7 an issue), the math pipe (1.1) and barriers (0.7).  Dims off 64 at
+// 128 x 128 spill 430 bytes as well.  24 rows x 4096 at 64 x 64 take 115 us
+// (0.9 TB/s), 3 x 5 x 1023 at 40 x 104 with gradients 120 to 145 us (as its lengths
+// fall); fp32 multiplications without the tensor cores took 242 and 363.
 template <int DX, int DZ, bool STATES, bool FULL>
 __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCtas)) la_f32(const __grid_constant__ Args a) {
     using S = Shape<DX, DZ>;
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__((Shape<DX, DZ>::kThreads), (Shape<DX, DZ>::kCt
         }
         if (STATES || ch + 1 < nch || (!at.split && p.s_out)) {
             // S <- a^L S + s_u sum_j a^(..) y_j^T z_j
-            constexpr int kSteps = FULL ? 2 : 1;  // into one u; with the conditions on tiles beside it, two spill
+            constexpr int kSteps = FULL ? 2 : 1;  // into one u; with the conditions on tiles beside it, two spill more (496 bytes, one 428)
             const float2 fl = a.decay[h * kLaPowers + L];
 #pragma unroll
             for (int m = 0; m < MT; ++m)

@@ -35,14 +35,14 @@
 // of code and ran at the rate of its instruction misses.
 //
 // Rounded to bf16 once each: P' and the copy of S that inter reads (each off by
-// 2^-9 of its values, like the operands beside them), and the outputs.  la_main's
+// up to 2^-8 of a value), and the outputs: 2.4e-3 in the 2-norm, 1.7e-3 of it theirs.  la_main's
 // own S stays in the accumulator: what its truncation (7e-6 over 256 chunks) and a
 // decay rounded to fp32 (2^-25 a chunk) cost is far below that.
 //
 // Bound by shared memory (operands of the products, tiles in and out, P' and the
 // split: 4500 cycles of it a chunk of 128 x 128, which takes 5900) and, in long
-// runs, by power.  16 heads x 32768 tokens x 128: la_states 73 us (3.7 TB/s),
-// la_main 115 us (4.5 TB/s), each alone; the call 181 us, 218 at the 1.56 GHz
+// runs, by power.  16 heads x 32768 tokens x 128: la_states 71 us (3.8 TB/s),
+// la_main 114 us (4.7 TB/s), each alone; the call 182 us, 218 at the 1.56 GHz
 // that the power limit leaves.
 #include <cuda.h>
 #include <cuda_bf16.h>
