@@ -448,7 +448,8 @@ la_step(const LaStep c, int H, int dk, int dv, const float2* __restrict__ decay)
             if (d < dk) s[i] = st[d * nv + col];
         }
     }
-    // rows that share a slot are taken in row order, by the first of them
+    // rows that share a slot are taken in row order, by the first of them (the others may have loaded its state while it
+    // was being stored, and drop it)
     bool more = false;
     if (c.slots) {
         int before = 0, after = 0;

@@ -597,6 +597,8 @@ FFTCONV_API fftconv_status fftconv_linattn_device_status(fftconv_linattn* plan, 
  *                          m = 0.1 ln(factor) + 1.
  * m = 1 otherwise.  Angles are reduced modulo a turn without loss; what is left is
  * the rounding of f_i to 2^-65 turn, times the position (2^-34 turn at 2^31).
+ * FFTCONV_ERR_UNSUPPORTED for calls of B N dim > 2^39 elements a head or more than
+ * 65535 heads, together.
  */
 typedef enum {
     FFTCONV_ROTARY_NONE = 0,
@@ -643,6 +645,7 @@ FFTCONV_API fftconv_status fftconv_rotary_apply(const fftconv_rotary* plan, cons
  * each head of [..][heads][C]).  Statistics in fp32: eps is zero or an fp32
  * number after rounding, and with zero a row of one value gives NaN, as 0 / 0.
  * `rows` of a call is at most the plan's and a multiple of groups.
+ * FFTCONV_ERR_UNSUPPORTED for other C, more than 65535 groups or 2^31 - 1 rows.
  */
 #define FFTCONV_NORM_MAX_C 16384
 FFTCONV_API fftconv_status fftconv_norm_plan_create(fftconv_norm** plan, int64_t rows, int C, int groups,
