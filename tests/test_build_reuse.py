@@ -106,3 +106,15 @@ def test_a_compilation_cut_short(tree, monkeypatch):
         made()
     monkeypatch.delenv("FAIL")
     assert made() == ["b.cu.o", "lib.so.tmp"]
+
+
+def test_without_a_compiler(tree, monkeypatch):
+    """A library that came with the tree is taken as it is, unless a source is newer."""
+    made, csrc = tree
+    made()
+    monkeypatch.setattr(build, "NVCC", str(csrc / "no-nvcc"))
+    assert made() == []
+    later = time.time() + 5
+    os.utime(csrc / "b.cu", (later, later))
+    with pytest.raises(OSError):
+        made()
